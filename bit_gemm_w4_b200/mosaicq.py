@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libmosaicq.so")
 OK, INVALID_ARG, UNSUPPORTED, OUT_OF_MEMORY, CUDA, DEVICE_TIMEOUT = range(6)
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = range(3)
 UNFUSED_NOALLOC_MAX_OUTPUTS = 2 * 1024 * 1024  # MQ_UNFUSED_NOALLOC_MAX_OUTPUTS
+FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}  # mq_fp4_format
 _PATHS = {"auto": PATH_AUTO, "decode": PATH_DECODE, "prefill": PATH_PREFILL}
 
 
@@ -53,6 +54,11 @@ class _Info(ctypes.Structure):
                 ("device_bytes", ctypes.c_int64), ("max_row_nnz", ctypes.c_int64)]
 
 
+class _Fp4Info(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("format", ctypes.c_int32), ("device", ctypes.c_int32), ("device_bytes", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libmosaicq.so is not built ({LIB_PATH}); run "
@@ -83,6 +89,21 @@ def _load():
         "mq_export_blocks": ([vp, vp, vp, vp, ctypes.POINTER(i64)], st),
         "mq_block_tiles_host": ([ctypes.POINTER(_Decomp), vp, vp, vp, ctypes.POINTER(i64)], st),
         "mq_device_error": ([vp, vp, ctypes.POINTER(ctypes.c_int32)], st),
+        "mq_fp4_code_bytes": ([i64], i64),
+        "mq_fp4_scale_bytes": ([st, i64], i64),
+        "mq_fp4_quantize": ([vp, st, i64, i64, i64, vp, i64, st, vp, vp, vp, vp], st),
+        "mq_fp4_dequantize": ([vp, vp, vp, i64, i64, st, vp, st, i64, vp], st),
+        "mq_fp4_pack": ([vp, st, i64, i64, i64, st, vp, ctypes.POINTER(vp)], st),
+        "mq_fp4_pack_codes": ([vp, vp, vp, i64, i64, i64, st, vp, ctypes.POINTER(vp)], st),
+        "mq_fp4_free": ([vp], None),
+        "mq_fp4_get_info": ([vp, ctypes.POINTER(_Fp4Info)], st),
+        "mq_fp4_export": ([vp, vp, vp, vp, vp], st),
+        "mq_fp4_workspace_bytes": ([vp, i64], i64),
+        "mq_fp4_linear": ([vp, vp, st, i64, i64, vp, i64, vp, ctypes.c_size_t, vp], st),
+        "mq_fp4_linear_codes": ([vp, vp, vp, vp, i64, vp, st, i64, vp], st),
+        "mq_fp4_linear_grouped": ([vp, vp, st, i64, i64, vp, i64, vp, vp, i64, vp, ctypes.c_size_t, vp], st),
+        "mq_fp4_linear_grouped_codes": ([vp, vp, vp, vp, i64, vp, vp, st, i64, vp], st),
+        "mq_fp4_device_error": ([vp, vp, ctypes.POINTER(ctypes.c_int32)], st),
         "mq_strerror": ([st], ctypes.c_char_p),
         "mq_last_error": ([], ctypes.c_char_p),
     }
@@ -417,6 +438,317 @@ class Weight:
     def free(self):
         if self._h:
             _lib.mq_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------- fp4
+# Microscaled 4-bit floating point (mq_fp4_*).
+
+_DTYPES = {}  # torch dtype -> mq_dtype, filled when torch is first needed
+
+
+def _dtype(t, where: str, fp32: bool = False) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    d = _DTYPES.get(t)
+    if d is None or (d == 2 and not fp32):
+        raise ValueError(f"{where}: unsupported dtype {t}")
+    return d
+
+
+def _fmt(fmt) -> int:
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"fp4 format must be one of {sorted(FP4_FORMATS)}, not {fmt!r}")
+    return FP4_FORMATS[fmt]
+
+
+class _On:
+    """A call's device and stream (None: the device's current stream) made
+    current while it runs, so that what the call allocates and converts
+    belongs to that stream too."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"a CUDA tensor is needed, not one on {device}")
+        self.cuda, self.device, self.given = torch.cuda, device, stream
+
+    def __enter__(self):
+        cuda = self.cuda
+        self.prev = cuda.current_device()
+        self.index = self.prev if self.device.index is None else self.device.index
+        if self.index != self.prev:
+            cuda.set_device(self.index)
+        self.was = None
+        current = cuda.current_stream()
+        self.stream = current.cuda_stream
+        if self.given is not None and _stream(self.given) != self.stream:
+            self.stream = _stream(self.given)
+            self.was = current
+            cuda.set_stream(self.given if isinstance(self.given, cuda.Stream) else
+                            cuda.ExternalStream(self.stream) if self.stream else cuda.default_stream())
+        return self
+
+    def __exit__(self, *exc):
+        if self.was is not None:
+            self.cuda.set_stream(self.was)
+        if self.index != self.prev:
+            self.cuda.set_device(self.prev)
+
+
+def _rows_view(X, where: str):
+    """A [rows, K] tensor whose rows are contiguous, and its row stride."""
+    if X.dim() != 2 or X.shape[1] < 1:
+        raise ValueError(f"{where}: a 2-D tensor with at least one column is needed")
+    M, K = X.shape
+    if (X.stride(1) != 1 and K > 1) or (X.stride(0) < K and M > 1):
+        X = X.contiguous()
+    return X, (X.stride(0) if M > 1 else K)
+
+
+def _index(t, device, where: str):
+    import torch
+    if t.device != device or t.dim() != 1 or t.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"{where} must be a 1-D int32 or int64 tensor on {device}")
+    if t.dtype == torch.int64:  # what int32 cannot hold is out of range either way
+        t = t.clamp(-1, 2**31 - 1).to(torch.int32)
+    return t.contiguous()
+
+
+class Fp4Tensor:
+    """A matrix of microscaled 4-bit values: uint8 codes and scales, a row
+    each (layout in mosaicq.h), and for nvfp4 the rows' fp32 factors."""
+
+    __slots__ = ("codes", "scales", "row_scale", "K", "fmt")
+
+    def __init__(self, codes, scales, row_scale, K: int, fmt: str):
+        import torch
+        f = _fmt(fmt)
+        K = int(K)
+        want = (_lib.mq_fp4_code_bytes(K), _lib.mq_fp4_scale_bytes(f, K))
+        if not want[0]:
+            raise ValueError("K must be in [1, 2^24]")
+        for t, name, width in ((codes, "codes", want[0]), (scales, "scales", want[1])):
+            if t.dtype != torch.uint8 or t.dim() < 2 or t.shape[-1] != width or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous uint8 [..., {width}] tensor")
+        if codes.shape[:-1] != scales.shape[:-1] or codes.device != scales.device:
+            raise ValueError("codes and scales must have the same rows and device")
+        if (row_scale is None) != (fmt == "mxfp4"):
+            raise ValueError("row_scale belongs to nvfp4, and only to it")
+        if row_scale is not None and (row_scale.dtype != torch.float32 or row_scale.shape != codes.shape[:-1] or
+                                      not row_scale.is_contiguous() or row_scale.device != codes.device):
+            raise ValueError("row_scale must be a contiguous float32 tensor, one value for each row")
+        self.codes, self.scales, self.row_scale, self.K, self.fmt = codes, scales, row_scale, K, fmt
+
+    @property
+    def rows(self) -> int:
+        return self.codes.numel() // self.codes.shape[-1]
+
+    @classmethod
+    def empty(cls, rows: int, K: int, fmt: str, device) -> "Fp4Tensor":
+        import torch
+        f = _fmt(fmt)
+        q = cls.__new__(cls)
+        q.codes = torch.empty((rows, _lib.mq_fp4_code_bytes(K)), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((rows, _lib.mq_fp4_scale_bytes(f, K)), dtype=torch.uint8, device=device)
+        q.row_scale = torch.empty(rows, dtype=torch.float32, device=device) if f else None
+        q.K, q.fmt = K, fmt
+        return q
+
+    def _ptrs(self):
+        r = self.row_scale
+        return self.codes.data_ptr(), self.scales.data_ptr(), None if r is None else r.data_ptr()
+
+    def dequantize(self, dtype=None, *, stream=None):
+        """The values as a [rows, K] tensor (fp32 unless a dtype is given)."""
+        import torch
+        d = _dtype(torch.float32 if dtype is None else dtype, "dequantize", fp32=True)
+        with _On(self.codes.device, stream) as on:
+            Y = torch.empty((self.rows, self.K), dtype=dtype or torch.float32, device=self.codes.device)
+            _check(_lib.mq_fp4_dequantize(*self._ptrs(), self.rows, self.K, FP4_FORMATS[self.fmt], Y.data_ptr(), d,
+                                          self.K, on.stream), "mq_fp4_dequantize")
+        return Y
+
+
+def fp4_quantize(X, fmt: str = "nvfp4", *, rows=None, stream=None) -> Fp4Tensor:
+    """X [M, K] (bf16, fp16 or fp32, any row stride) as microscaled 4-bit
+    floating point. With rows (1-D integer tensor) output row r is X[rows[r]],
+    and zeros where rows[r] is no row of X."""
+    f = _fmt(fmt)
+    d = _dtype(X.dtype, "fp4_quantize", fp32=True)
+    with _On(X.device, stream) as on:
+        X, ldx = _rows_view(X, "fp4_quantize")
+        if rows is not None:
+            rows = _index(rows, X.device, "rows")
+        M = X.shape[0] if rows is None else rows.shape[0]
+        q = Fp4Tensor.empty(M, X.shape[1], fmt, X.device)
+        _check(_lib.mq_fp4_quantize(X.data_ptr(), d, M, X.shape[1], ldx, None if rows is None else rows.data_ptr(),
+                                    X.shape[0], f, *q._ptrs(), on.stream), "mq_fp4_quantize")
+    return q
+
+
+class Fp4Weight:
+    """E packed matrices [N, K] of microscaled 4-bit values on one CUDA device
+    (owns its device buffers): a linear layer (E = 1) or a layer's experts."""
+
+    def __init__(self, handle: int):
+        import torch
+        self._h = handle
+        i = _Fp4Info()
+        _check(_lib.mq_fp4_get_info(handle, ctypes.byref(i)), "mq_fp4_get_info")
+        self.E, self.N, self.K, self.device_bytes = i.E, i.N, i.K, i.device_bytes
+        self.fmt = {v: k for k, v in FP4_FORMATS.items()}[i.format]
+        self.device = torch.device("cuda", i.device)
+
+    @classmethod
+    def pack(cls, W, fmt: str = "nvfp4", *, stream=None) -> "Fp4Weight":
+        """Quantise and pack a CUDA tensor W [N, K] or [E, N, K] (bf16, fp16
+        or fp32)."""
+        f = _fmt(fmt)
+        d = _dtype(W.dtype, "Fp4Weight.pack", fp32=True)
+        if W.dim() not in (2, 3):
+            raise ValueError("W must be [N, K] or [E, N, K]")
+        h = ctypes.c_void_p()
+        with _On(W.device, stream) as on:
+            W = W.contiguous()
+            E = W.shape[0] if W.dim() == 3 else 1
+            _check(_lib.mq_fp4_pack(W.data_ptr(), d, E, W.shape[-2], W.shape[-1], f, on.stream, ctypes.byref(h)),
+                   "mq_fp4_pack")
+        return cls(h.value)
+
+    @classmethod
+    def pack_codes(cls, codes, scales, row_scale, K: int, fmt: str, *, stream=None) -> "Fp4Weight":
+        """Pack codes [N, .] or [E, N, .] as they are (CUDA tensors in the
+        layout of Fp4Tensor)."""
+        q = Fp4Tensor(codes, scales, row_scale, K, fmt)
+        if codes.dim() not in (2, 3):
+            raise ValueError("codes must be [N, .] or [E, N, .]")
+        h = ctypes.c_void_p()
+        with _On(codes.device, stream) as on:
+            E = codes.shape[0] if codes.dim() == 3 else 1
+            _check(_lib.mq_fp4_pack_codes(*q._ptrs(), E, codes.shape[-2], q.K, FP4_FORMATS[fmt], on.stream,
+                                          ctypes.byref(h)), "mq_fp4_pack_codes")
+        return cls(h.value)
+
+    @property
+    def handle(self) -> int:
+        return self._h
+
+    def workspace_bytes(self, rows: int) -> int:
+        return int(_lib.mq_fp4_workspace_bytes(self._h, rows))
+
+    def export(self, *, stream=None) -> Fp4Tensor:
+        """The packed matrices as one quantised [E * N, K] matrix."""
+        with _On(self.device, stream) as on:
+            q = Fp4Tensor.empty(self.E * self.N, self.K, self.fmt, self.device)
+            _check(_lib.mq_fp4_export(self._h, *q._ptrs(), on.stream), "mq_fp4_export")
+        return q
+
+    def _output(self, Y, rows: int, dtype):
+        import torch
+        if Y is None:
+            Y = torch.empty((rows, self.N), dtype=dtype, device=self.device)
+        elif Y.device != self.device or Y.dtype != dtype or Y.shape != (rows, self.N) or \
+                (Y.stride(1) != 1 and self.N > 1) or (Y.stride(0) < self.N and rows > 1):
+            raise ValueError(f"Y must be a {dtype} [{rows}, {self.N}] tensor on {self.device} with contiguous rows")
+        return Y, (Y.stride(0) if rows > 1 else self.N)
+
+    def _workspace(self, workspace, rows: int):
+        import torch
+        if workspace is None:
+            workspace = torch.empty(max(16, self.workspace_bytes(rows)), dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
+        return workspace
+
+    def _quantized(self, X: Fp4Tensor, dtype):
+        import torch
+        if X.fmt != self.fmt or X.K != self.K or X.codes.device != self.device:
+            raise ValueError(f"the activations must be {self.fmt} with K = {self.K} on {self.device}")
+        dtype = torch.bfloat16 if dtype is None else dtype
+        return dtype, _dtype(dtype, "the output")
+
+    def linear(self, X, Y=None, workspace=None, *, dtype=None, stream=None):
+        """Y = X @ W^T. X: a bf16 or fp16 [M, K] tensor, quantised within the
+        call into the workspace (workspace_bytes(M) bytes), with Y of its
+        type; or an Fp4Tensor, with Y of `dtype` (bf16 unless given)."""
+        if isinstance(X, Fp4Tensor):
+            dtype, d = self._quantized(X, dtype)
+            with _On(self.device, stream) as on:
+                Y, ldy = self._output(Y, X.rows, dtype)
+                _check(_lib.mq_fp4_linear_codes(self._h, *X._ptrs(), X.rows, Y.data_ptr(), d, ldy, on.stream),
+                       "mq_fp4_linear_codes")
+            return Y
+        with _On(self.device, stream) as on:
+            X, d, ldx = self._input(X, dtype)
+            M = X.shape[0]
+            Y, ldy = self._output(Y, M, X.dtype)
+            workspace = self._workspace(workspace, M)
+            _check(_lib.mq_fp4_linear(self._h, X.data_ptr(), d, M, ldx, Y.data_ptr(), ldy, workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), on.stream), "mq_fp4_linear")
+        return Y
+
+    def linear_grouped(self, X, offsets, Y=None, workspace=None, *, rows=None, dtype=None, stream=None):
+        """The experts' products: Y[r] = x[r] @ W[e]^T for offsets[e] <= r <
+        offsets[e + 1] (offsets: E + 1 integers on the device). x[r] is
+        X[rows[r]], or X[r] without rows; X as for linear. Rows of Y that
+        belong to no expert are left as they were (undefined in a Y that the
+        call makes)."""
+        if offsets.dim() != 1 or offsets.shape[0] != self.E + 1:
+            raise ValueError(f"offsets must hold E + 1 = {self.E + 1} values")
+        if isinstance(X, Fp4Tensor):
+            if rows is not None:
+                raise ValueError("rows are taken when X is quantised: fp4_quantize(X, rows=rows)")
+            dtype, d = self._quantized(X, dtype)
+            with _On(self.device, stream) as on:
+                offsets = _index(offsets, self.device, "offsets")
+                Y, ldy = self._output(Y, X.rows, dtype)
+                _check(_lib.mq_fp4_linear_grouped_codes(self._h, *X._ptrs(), X.rows, offsets.data_ptr(),
+                                                        Y.data_ptr(), d, ldy, on.stream),
+                       "mq_fp4_linear_grouped_codes")
+            return Y
+        with _On(self.device, stream) as on:
+            X, d, ldx = self._input(X, dtype)
+            offsets = _index(offsets, self.device, "offsets")
+            if rows is not None:
+                rows = _index(rows, self.device, "rows")
+            R = X.shape[0] if rows is None else rows.shape[0]
+            Y, ldy = self._output(Y, R, X.dtype)
+            workspace = self._workspace(workspace, R)
+            _check(_lib.mq_fp4_linear_grouped(self._h, X.data_ptr(), d, X.shape[0], ldx,
+                                              None if rows is None else rows.data_ptr(), R, offsets.data_ptr(),
+                                              Y.data_ptr(), ldy, workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size(), on.stream),
+                   "mq_fp4_linear_grouped")
+        return Y
+
+    def _input(self, X, dtype):
+        if dtype is not None and dtype != X.dtype:
+            raise ValueError("Y has the type of X; dtype is for quantised activations")
+        d = _dtype(X.dtype, "X")
+        if X.device != self.device or X.dim() != 2 or X.shape[1] != self.K:
+            raise ValueError(f"X must be a [rows, {self.K}] tensor on {self.device}")
+        X, ldx = _rows_view(X, "X")
+        return X, d, ldx
+
+    def device_error(self, stream=None) -> int:
+        code = ctypes.c_int32()
+        with _On(self.device, stream) as on:
+            st = _lib.mq_fp4_device_error(self._h, on.stream, ctypes.byref(code))
+        if st not in (OK, DEVICE_TIMEOUT):
+            _check(st, "mq_fp4_device_error")
+        return code.value
+
+    def free(self):
+        if self._h:
+            _lib.mq_fp4_free(self._h)
             self._h = None
 
     def __del__(self):

@@ -373,6 +373,129 @@ mq_status mq_export_blocks(const mq_weight *w, int32_t *blk_ptr, uint16_t *blk_c
  * Synchronizes `stream`. Returns MQ_ERR_DEVICE_TIMEOUT when non-zero. */
 mq_status mq_device_error(const mq_weight *w, mq_stream stream, int32_t *code);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (mq_fp4_*): operands of the tensor cores'
+ * block-scaled 4-bit MMAs, for weights and activations alike.
+ *
+ * An element is an E2M1 code: sign (bit 3) and a magnitude of 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 (codes 0..7). A block of consecutive columns of a row shares a
+ * scale. All roundings are to nearest even, in 32 bits; max |.| runs over the
+ * block (the row) with zeros past K.
+ *   MQ_FP4_MX  blocks of 32, scale 2^(s - 127) with a byte s. With E the
+ *              exponent field of max |block| as a 32-bit float, s = max(E - 2,
+ *              0); code = e2m1(x * 2^(127 - s)), saturating at 6. A block with
+ *              an infinity or a NaN gets s = 255 (NaN) and codes 0.
+ *   MQ_FP4_NV  blocks of 16, scale b in e4m3 (a byte without sign), and a
+ *              32-bit factor r for each row: r = max(max |row| * (1 / 2688),
+ *              2^-100), b = e4m3((max |block| * (1 / 6)) * (1 / r)), code =
+ *              e2m1(x * (1 / (b * r))), codes 0 where b is 0. A row with an
+ *              infinity or a NaN gets r = NaN, scales 0 and codes 0.
+ * value = e2m1(code) * scale (* r).
+ *
+ * A quantised matrix is held row by row, on the device:
+ *   codes      [rows][mq_fp4_code_bytes(K)] = 16 * ceil(K / 32) bytes a row,
+ *              the even column of a pair in the low nibble;
+ *   scales     [rows][mq_fp4_scale_bytes(fmt, K)] bytes a row: one for each
+ *              block, padded to a multiple of 16 bytes;
+ *   row_scale  float [rows] (MQ_FP4_NV; NULL for MQ_FP4_MX).
+ * Codes and scales past K must be 0 (mq_fp4_quantize writes them so), and
+ * codes and scales 16-byte aligned. */
+typedef enum { MQ_FP4_MX = 0, MQ_FP4_NV = 1 } mq_fp4_format;
+typedef enum { MQ_BF16 = 0, MQ_FP16 = 1, MQ_FP32 = 2 } mq_dtype;
+typedef struct mq_fp4_weight mq_fp4_weight; /* opaque; owns E packed matrices on one GPU */
+
+typedef struct {
+    int64_t E, N, K;      /* matrices of N rows (output features) and K columns */
+    int32_t format;       /* mq_fp4_format */
+    int32_t device;
+    int64_t device_bytes; /* device memory the handle owns */
+} mq_fp4_info;
+
+/* Bytes of a row of codes / scales; 0 for a K outside [1, 2^24] or an unknown
+ * format. */
+int64_t mq_fp4_code_bytes(int64_t K);
+int64_t mq_fp4_scale_bytes(mq_fp4_format fmt, int64_t K);
+
+/* Quantise `rows` rows of X (bf16, fp16 or fp32, row stride ldx >= K elements,
+ * x_rows rows, aligned to its elements). Output row r is X row index[r]
+ * (int32, device), or X row r when index is NULL (then rows == x_rows). A row
+ * whose index lies outside [0, x_rows) is a row of zeros. Asynchronous, no
+ * allocation.
+ * Errors: INVALID_ARG for an unknown format or dtype, K outside [1, 2^24],
+ * negative counts, ldx < K, NULL or misaligned buffers; UNSUPPORTED above
+ * 2^30 rows; CUDA when the launch fails. */
+mq_status mq_fp4_quantize(const void *X_dev, mq_dtype dtype, int64_t rows, int64_t K, int64_t ldx,
+                          const int32_t *index, int64_t x_rows, mq_fp4_format fmt, void *codes,
+                          void *scales, float *row_scale, mq_stream stream);
+
+/* The values of a quantised matrix, rounded once to dtype, into Y (row stride
+ * ldy >= K elements). Errors as mq_fp4_quantize. */
+mq_status mq_fp4_dequantize(const void *codes, const void *scales, const float *row_scale,
+                            int64_t rows, int64_t K, mq_fp4_format fmt, void *Y_dev, mq_dtype dtype,
+                            int64_t ldy, mq_stream stream);
+
+/* Pack E matrices W [E][N][K] (device memory, contiguous) for the products:
+ * mq_fp4_pack quantises bf16, fp16 or fp32 values, mq_fp4_pack_codes takes a
+ * quantised [E * N][K] matrix as it is. The handle holds its own copy. Both
+ * wait for the stream. Free with mq_fp4_free (NULL is ignored).
+ * Errors: as mq_fp4_quantize, plus INVALID_ARG for E or N <= 0, UNSUPPORTED
+ * for more than 65535 matrices or 2^30 rows in all, OUT_OF_MEMORY. */
+mq_status mq_fp4_pack(const void *W_dev, mq_dtype dtype, int64_t E, int64_t N, int64_t K,
+                      mq_fp4_format fmt, mq_stream stream, mq_fp4_weight **out);
+mq_status mq_fp4_pack_codes(const void *codes, const void *scales, const float *row_scale, int64_t E,
+                            int64_t N, int64_t K, mq_fp4_format fmt, mq_stream stream,
+                            mq_fp4_weight **out);
+void mq_fp4_free(mq_fp4_weight *w);
+mq_status mq_fp4_get_info(const mq_fp4_weight *w, mq_fp4_info *out);
+
+/* The packed matrices as one quantised [E * N][K] matrix, into device buffers
+ * of the caller; the inverse of mq_fp4_pack_codes. Asynchronous. */
+mq_status mq_fp4_export(const mq_fp4_weight *w, void *codes, void *scales, float *row_scale,
+                        mq_stream stream);
+
+/* Device bytes the products below need to quantise `rows` rows. */
+int64_t mq_fp4_workspace_bytes(const mq_fp4_weight *w, int64_t rows);
+
+/* Y = X W^T for a handle of one matrix: X [M][K] (bf16 or fp16, stride ldx)
+ * is quantised to the weight's format into `workspace` (16-byte aligned, at
+ * least mq_fp4_workspace_bytes(w, M), not shared with a concurrent call) and
+ * multiplied on the tensor cores' 4-bit path: exact products of codes and
+ * scales, fp32 accumulation, Y [M][N] of X's type, stride ldy >= N, each
+ * element rounded once. Asynchronous, no allocation; results do not depend on
+ * timing. Y must not overlap X or the workspace. M = 0 launches nothing.
+ * mq_fp4_linear_codes takes X already quantised to the weight's format, for
+ * an X that several weights share.
+ * Errors: INVALID_ARG for NULL, misaligned or too small buffers, strides
+ * below the widths, a handle of several matrices or a current device other
+ * than the handle's; UNSUPPORTED for fp32 or more than 2^30 rows; CUDA when a
+ * launch fails. */
+mq_status mq_fp4_linear(const mq_fp4_weight *w, const void *X_dev, mq_dtype dtype, int64_t M,
+                        int64_t ldx, void *Y_dev, int64_t ldy, void *workspace,
+                        size_t workspace_bytes, mq_stream stream);
+mq_status mq_fp4_linear_codes(const mq_fp4_weight *w, const void *codes, const void *scales,
+                              const float *row_scale, int64_t M, void *Y_dev, mq_dtype dtype,
+                              int64_t ldy, mq_stream stream);
+
+/* The products of a mixture of experts: R rows grouped by matrix, Y[r] =
+ * x[r] W[e]^T for offsets[e] <= r < offsets[e + 1] (offsets: int32 [E + 1],
+ * device, ascending within [0, R]; out-of-range or descending entries are
+ * clamped to that, never followed outside the buffers). x[r] is X row
+ * index[r], or X row r when index is NULL, as in mq_fp4_quantize. Rows of Y
+ * outside [offsets[0], offsets[E]) are left as they were. Workspace for R
+ * rows. The device reads the offsets; the host does not wait for them.
+ * mq_fp4_linear_grouped_codes takes the R rows already quantised.
+ * Errors as mq_fp4_linear, plus INVALID_ARG for NULL offsets. */
+mq_status mq_fp4_linear_grouped(const mq_fp4_weight *w, const void *X_dev, mq_dtype dtype,
+                                int64_t x_rows, int64_t ldx, const int32_t *index, int64_t R,
+                                const int32_t *offsets, void *Y_dev, int64_t ldy, void *workspace,
+                                size_t workspace_bytes, mq_stream stream);
+mq_status mq_fp4_linear_grouped_codes(const mq_fp4_weight *w, const void *codes, const void *scales,
+                                      const float *row_scale, int64_t R, const int32_t *offsets,
+                                      void *Y_dev, mq_dtype dtype, int64_t ldy, mq_stream stream);
+
+/* Read and clear an fp4 handle's device error word, as mq_device_error. */
+mq_status mq_fp4_device_error(const mq_fp4_weight *w, mq_stream stream, int32_t *code);
+
 /* Static text for a status code. */
 const char *mq_strerror(mq_status s);
 

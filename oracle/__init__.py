@@ -18,6 +18,8 @@ the MosaicQuant pages:
   * w4a4.py      - the W4A4 variant: per-token int4 activation quantization
     (the pipeline's quantization stage in "Methodology" 3.) and the product
     from exact integer sums ("Experimental Results" evaluate W4A4).
+  * fp4.py       - microscaled 4-bit floating point: quantisation, the values
+    held, and the product.
 
 This package is test infrastructure. Only tests/, __graft_entry__.smoke() and
 bench.py's CPU-baseline / reference arm may import it. The product path
