@@ -425,6 +425,19 @@ bool encode_bytes_map(CUtensorMap *map, const void *base, int64_t pitch, int64_t
     return r == CUDA_SUCCESS;
 }
 
+bool encode_pieces_map(CUtensorMap *map, const void *base, int64_t bytes, int box_bytes) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(bytes / 256)};
+    cuuint64_t strides[1] = {256};
+    cuuint32_t box[2] = {256, static_cast<cuuint32_t>(box_bytes / 256)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace mq
 
 using namespace mq;

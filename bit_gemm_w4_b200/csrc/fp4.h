@@ -49,7 +49,8 @@ struct Fp4Device {
     uint8_t *scales = nullptr;
     float *row_scale = nullptr;  // [E][N], NULL for MQ_FP4_MX
     int *err = nullptr;
-    CUtensorMap map;  // codes as [E][N][pitch] bytes, boxes of 128 rows x 128 bytes
+    CUtensorMap map;        // codes as [E][N][pitch] bytes, boxes of 128 rows x 128 bytes
+    CUtensorMap scale_map;  // scales as rows of 256 bytes, boxes of one piece
 };
 
 // Bytes of one piece of `scales` above.
@@ -76,10 +77,18 @@ mq_status launch_fp4_scale_order(const Fp4Device &d, uint8_t *row_major, bool to
 mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                             mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
 
+// The form of launch_fp4_linear for many tokens (fp4_wide.cu).
+mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
+                          mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
+
 // Byte matrix [outer][rows][pitch] (outer = 0: [rows][pitch], two coordinates)
 // as a tensor map with boxes of box_rows x 128 bytes, 128-byte swizzle, zero
 // fill.
 bool encode_bytes_map(CUtensorMap *map, const void *base, int64_t pitch, int64_t rows, int64_t outer,
                       int box_rows);
+
+// `bytes` (a multiple of 256) as a tensor map of rows of 256 bytes with boxes
+// of box_bytes, in their order in memory.
+bool encode_pieces_map(CUtensorMap *map, const void *base, int64_t bytes, int box_bytes);
 
 }  // namespace mq

@@ -99,7 +99,8 @@ mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
     if (fmt == MQ_FP4_NV)
         if (mq_status st = get(reinterpret_cast<void **>(&d.row_scale), E * N * 4)) return st;
     if (mq_status st = get(reinterpret_cast<void **>(&d.err), 4)) return st;
-    if (!encode_bytes_map(&d.map, d.codes, d.pitch, N, E, 128))
+    if (!encode_bytes_map(&d.map, d.codes, d.pitch, N, E, 128) ||
+        !encode_pieces_map(&d.scale_map, d.scales, E * d.NT * d.KS * fp4_piece_bytes(fmt), fp4_piece_bytes(fmt)))
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the weight");
     return MQ_OK;
 }

@@ -1,0 +1,134 @@
+// Device helpers that the fp4 products share: where a tile lies, the store of
+// an output, waits and arrivals across a cluster.
+#pragma once
+
+#include "common.cuh"
+#include "tc5.cuh"
+
+namespace mq {
+
+// ~1 ms, far beyond any copy's time: what a block that gave up a wait leaves
+// its copies in flight to land before it hands its shared memory back.
+constexpr long long kDrainCycles = 1 << 21;
+
+__device__ __forceinline__ void drain_after_abort(const int *abort_flag) {
+    if (!*reinterpret_cast<const volatile int *>(abort_flag)) return;
+    const long long t0 = clock64();
+    while (clock64() - t0 < kDrainCycles) {
+    }
+}
+
+// Tiles in order: matrix by matrix, each with ceil(rows / TT) token tiles for
+// each of its NT row tiles; the token tiles of one row tile are neighbours,
+// so that its codes come from L2 again. Each warp walks for itself (all lanes
+// together) over ascending tile indices.
+struct Tile {
+    int e, m0, tokens, nt;
+};
+
+struct TileWalk {
+    const int32_t *offsets;  // NULL: one matrix with all R rows
+    int E, R, TT, NT;
+    int base = 0;            // matrices [base, base + 32) hold the next tile, or later ones do
+    long long before = 0;    // tiles of the matrices below base
+
+    __device__ __forceinline__ TileWalk(const int32_t *o, int e, int r, int tt, int nt)
+        : offsets(o), E(e), R(r), TT(tt), NT(nt) {}
+
+    __device__ __forceinline__ bool find(long long t, Tile &out) {
+        if (!offsets) {
+            const int tiles = (R + TT - 1) / TT;
+            if (t >= static_cast<long long>(tiles) * NT) return false;
+            const int tt = static_cast<int>(t % tiles);
+            out = {0, tt * TT, min(TT, R - tt * TT), static_cast<int>(t / tiles)};
+            return true;
+        }
+        const int lane = threadIdx.x & 31;
+        while (base < E) {
+            const int e = base + lane;
+            int a = 0, b = 0;
+            if (e < E) {
+                // entries out of range or order are clamped, never followed
+                a = min(max(__ldg(offsets + e), 0), R);
+                b = min(max(__ldg(offsets + e + 1), a), R);
+            }
+            const long long mine = static_cast<long long>((b - a + TT - 1) / TT) * NT;
+            long long sum = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const long long o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, t - before < sum);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                a = __shfl_sync(0xffffffffu, a, l);
+                b = __shfl_sync(0xffffffffu, b, l);
+                const long long within = t - before - __shfl_sync(0xffffffffu, sum - mine, l);
+                const int tiles = (b - a + TT - 1) / TT;
+                const int tt = static_cast<int>(within % tiles);
+                out = {base + l, a + tt * TT, min(TT, b - a - tt * TT), static_cast<int>(within / tiles)};
+                return true;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+            base += 32;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ void store_output(void *Y, long long at, float y, bool fp16) {
+    if (fp16)
+        static_cast<__half *>(Y)[at] = __float2half_rn(y);
+    else
+        static_cast<__nv_bfloat16 *>(Y)[at] = __float2bfloat16_rn(y);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Bulk copy of `bytes` (a multiple of 16) into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The address, in the cluster's shared memory, of this CTA's `p` in CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// Arrives on a barrier given by in_cta. What this thread wrote for the tensor
+// core in its own shared memory has to be fenced (fence_proxy_async) before.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tiled loads into this CTA's shared memory that complete on a barrier of
+// either CTA of a pair (given by in_cta).
+__device__ __forceinline__ void tma_pair_load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_pair_load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+}  // namespace mq

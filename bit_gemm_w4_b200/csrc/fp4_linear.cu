@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "fp4.h"
+#include "fp4_device.cuh"
 #include "tc5.cuh"
 
 namespace mq {
@@ -29,7 +30,6 @@ constexpr int kThreads = 192;
 constexpr int kMaxStages = 8;
 constexpr int kBoxRows = 16;  // tokens of one copy
 constexpr int kATile = 128 * 128;
-constexpr long long kDrainCycles = 1 << 21;  // ~1 ms, far beyond any copy's time
 
 struct NarrowParams {
     CUtensorMap tw, tx;
@@ -60,39 +60,6 @@ struct NarrowSmem {
     __host__ __device__ static int total(int TT, int stages) { return slot(TT) * stages + 1024 + 256; }
 };
 
-// The matrix and token tile of tile index t: matrices in order, each with
-// ceil(rows / TT) * NT tiles. Run by one warp.
-__device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int R, int TT, int NT, long long t,
-                                          int &e_out, int &begin, int &end, long long &within) {
-    const int lane = threadIdx.x & 31;
-    for (int base = 0; base < E; base += 32) {
-        const int e = base + lane;
-        int a = 0, b = 0;
-        if (e < E) {
-            a = offsets ? min(max(__ldg(offsets + e), 0), R) : 0;
-            b = offsets ? min(max(__ldg(offsets + e + 1), a), R) : R;
-        }
-        const long long mine = static_cast<long long>((b - a + TT - 1) / TT) * NT;
-        long long sum = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const long long o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += o;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, t < sum);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            e_out = base + l;
-            begin = __shfl_sync(0xffffffffu, a, l);
-            end = __shfl_sync(0xffffffffu, b, l);
-            within = t - __shfl_sync(0xffffffffu, sum - mine, l);
-            return true;
-        }
-        t -= __shfl_sync(0xffffffffu, sum, 31);
-    }
-    return false;
-}
-
 template <bool NV>
 __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_constant__ NarrowParams p) {
     using S = NarrowSmem<NV>;
@@ -110,17 +77,14 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
 
     const int split = p.split, rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
     if (warp == 0) {
-        int e = 0, a = 0, b = 0;
-        long long within = 0;
-        const bool live = find_tile(p.offsets, p.E, p.R, TT, p.NT, blockIdx.x / split, e, a, b, within);
+        Tile t{0, 0, 0, 0};
+        TileWalk walk(p.offsets, p.E, p.R, TT, p.NT);
+        const bool live = walk.find(blockIdx.x / split, t);
         if (lane == 0) {
-            // token tiles of one row tile are neighbours, so that its codes come from L2 again
-            const int tiles = (b - a + TT - 1) / TT;
-            const int nt = live ? static_cast<int>(within / tiles) : 0, tt = live ? static_cast<int>(within % tiles) : 0;
-            info[0] = e;
-            info[1] = a + tt * TT;
-            info[2] = min(TT, b - a - tt * TT);
-            info[3] = nt;
+            info[0] = t.e;
+            info[1] = t.m0;
+            info[2] = t.tokens;
+            info[3] = t.nt;
             info[4] = live ? 1 : 0;
             for (int s = 0; s < stages; ++s) {
                 mbar_init(&full[s], 3);
@@ -146,53 +110,58 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
     if (!live) {
         // nothing to do
     } else if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t bytes = kATile + S::kScales + nb * kBoxRows * 128;
-            const uint8_t *ws = p.wscales + ((static_cast<long long>(expert) * p.NT + info[3]) * p.KS + k0) * S::kScales;
-            auto weight = [&](int i, int s) {
-                uint8_t *at = smem + s * slot;
-                mbar_arrive_expect_tx(&full[s], bytes);
-                tma_load_3d(at, &p.tw, &full[s], (k0 + i) * 128, n0, expert);
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                        smem_u32(at + kATile + TT * 128)),
-                    "l"(ws + static_cast<long long>(i) * S::kScales), "r"(S::kScales), "r"(smem_u32(&full[s]))
-                    : "memory");
-            };
-            auto tokens_in = [&](int i, int s) {
-                for (int b = 0; b < nb; ++b)
-                    tma_load_2d(smem + s * slot + kATile + b * kBoxRows * 128, &p.tx, &full[s], (k0 + i) * 128,
-                                m0 + b * kBoxRows);
-            };
-            // the weight does not depend on the launch before: its first stages go ahead
-            const int ahead = min(stages, nk);
+        const uint32_t bytes = kATile + S::kScales + nb * kBoxRows * 128;
+        const uint8_t *ws = p.wscales + ((static_cast<long long>(expert) * p.NT + info[3]) * p.KS + k0) * S::kScales;
+        auto weight = [&](int i, int s) {
+            uint8_t *at = smem + s * slot;
+            mbar_arrive_expect_tx(&full[s], bytes);
+            tma_load_3d(at, &p.tw, &full[s], (k0 + i) * 128, n0, expert);
+            bulk_load(at + kATile + TT * 128, ws + static_cast<long long>(i) * S::kScales, S::kScales, &full[s]);
+        };
+        auto tokens_in = [&](int i, int s) {
+            for (int b = 0; b < nb; ++b)
+                tma_load_2d(smem + s * slot + kATile + b * kBoxRows * 128, &p.tx, &full[s], (k0 + i) * 128,
+                            m0 + b * kBoxRows);
+        };
+        // the weight does not depend on the launch before: its first stages go ahead
+        const int ahead = min(stages, nk);
+        if (tc5::elect())
             for (int i = 0; i < ahead; ++i) weight(i, i);
-            pdl_wait();
+        __syncwarp();
+        pdl_wait();
+        if (tc5::elect())
             for (int i = 0; i < ahead; ++i) tokens_in(i, i);
-            for (int i = ahead, s = 0, ph = 0; i < nk; ++i) {
-                if (!mbar_wait(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag)) break;
+        __syncwarp();
+        bool ok = true;
+        for (int i = ahead, s = 0, ph = 0; i < nk && ok; ++i) {
+            ok = mbar_wait(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (tc5::elect()) {
                 weight(i, s);
                 tokens_in(i, s);
-                if (++s == stages) s = 0, ph ^= 1;
             }
+            __syncwarp();
+            if (++s == stages) s = 0, ph ^= 1;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t n = nb * kBoxRows;
-            const uint32_t desc = tc5::idesc(128, n, !NV);
-            const uint32_t sfa = tmem + TT, sfb = sfa + 4 * kUnits;
-            bool ok = true;
-            for (int i = 0, s = 0, ph = 0; i < nk && ok; ++i) {
-                ok = mbar_wait(&full[s], ph, p.err, kErrWaitFull, abort_flag);
-                tc5::fence_after();
-                const uint32_t at = smem_u32(smem + s * slot);
-                const uint32_t sa = at + kATile + TT * 128, sb = sa + S::kScales;
+        const uint32_t desc = tc5::idesc(128, nb * kBoxRows, !NV);
+        const uint32_t sfa = tmem + TT, sfb = sfa + 4 * kUnits;
+        bool ok = true;
+        for (int i = 0, s = 0, ph = 0; i < nk && ok; ++i) {
+            ok = mbar_wait(&full[s], ph, p.err, kErrWaitFull, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc5::fence_after();
+            const uint32_t at = smem_u32(smem) + s * slot;
+            const uint32_t sa = at + kATile + TT * 128, sb = sa + S::kScales;
+            const uint64_t da = tc5::operand_desc(at), db = tc5::operand_desc(at + kATile);
+            if (tc5::elect()) {
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) {
                     tc5::copy_scales<1>(sfa + 4 * u, tc5::scale_desc(sa + 512 * u));
                     tc5::copy_scales<1>(sfb + 4 * u, tc5::scale_desc(sb + 512 * u));
                 }
-                const uint64_t da = tc5::operand_desc(at), db = tc5::operand_desc(at + kATile);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int u = NV ? k : k >> 1;
@@ -201,10 +170,12 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
                                     sfb + 4 * u, i > 0 || k > 0);
                 }
                 tc5::commit(&empty[s]);
-                if (++s == stages) s = 0, ph ^= 1;
             }
-            tc5::commit(done);
+            __syncwarp();
+            if (++s == stages) s = 0, ph ^= 1;
         }
+        if (tc5::elect()) tc5::commit(done);
+        __syncwarp();
     } else if (warp < 4) {
         // the tokens' scales: 4-byte pieces into the tensor core's order. A
         // stage is handed over two iterations after its copies were issued.
@@ -257,8 +228,12 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
         const float fw = NV && n < p.N ? __ldg(p.wfactor + static_cast<long long>(expert) * p.N + n) : 1.0f;
         float *part = reinterpret_cast<float *>(smem);  // [tokens][128], the ring is drained
         for (int c = 0; c < nb * kBoxRows; c += 16) {
+            uint32_t bits[16];
+            tc5::load16(tmem + (static_cast<uint32_t>(quad) << 21) + c, bits);
+            tc5::load_wait();
             float v[16];
-            tc5::load16(tmem + (static_cast<uint32_t>(quad) << 21) + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(bits[j]);
             if (split > 1) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -270,22 +245,12 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
                     if (t >= tokens) break;
                     float y = v[j];
                     if constexpr (NV) y = y * p.xfactor[m0 + t] * fw;
-                    const long long at = (m0 + t) * p.ldy + n;
-                    if (p.fp16)
-                        static_cast<__half *>(p.Y)[at] = __float2half_rn(y);
-                    else
-                        static_cast<__nv_bfloat16 *>(p.Y)[at] = __float2bfloat16_rn(y);
+                    store_output(p.Y, (m0 + t) * p.ldy + n, y, p.fp16);
                 }
             }
         }
     }
-    if (live && *static_cast<volatile int *>(abort_flag)) {
-        // a wait was given up: copies in flight get time to land before the
-        // shared memory is given back
-        const long long t0 = clock64();
-        while (clock64() - t0 < kDrainCycles) {
-        }
-    }
+    drain_after_abort(abort_flag);
     __syncwarp();
     if (live && split > 1) {
         cluster_sync();
@@ -303,11 +268,7 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
                 if (n >= p.N) continue;
                 if constexpr (NV)
                     y = y * p.xfactor[m0 + t] * __ldg(p.wfactor + static_cast<long long>(expert) * p.N + n);
-                const long long at = (m0 + t) * p.ldy + n;
-                if (p.fp16)
-                    static_cast<__half *>(p.Y)[at] = __float2half_rn(y);
-                else
-                    static_cast<__nv_bfloat16 *>(p.Y)[at] = __float2bfloat16_rn(y);
+                store_output(p.Y, (m0 + t) * p.ldy + n, y, p.fp16);
             }
         }
         cluster_sync();
@@ -394,6 +355,8 @@ mq_status run_narrow(const Fp4Device &d, const Fp4Rows &x, const int32_t *offset
 mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                             mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream) {
     if (x.rows <= 0) return MQ_OK;
+    const int64_t per = offsets ? x.rows / std::min<int64_t>(d.E, x.rows) : x.rows;  // rows of a matrix
+    if (per > 128) return launch_fp4_wide(d, x, offsets, Y, dtype, ldy, chained, stream);
     return d.fmt == MQ_FP4_NV ? run_narrow<true>(d, x, offsets, Y, dtype, ldy, chained, stream)
                               : run_narrow<false>(d, x, offsets, Y, dtype, ldy, chained, stream);
 }

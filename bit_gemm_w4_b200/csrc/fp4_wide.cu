@@ -1,0 +1,440 @@
+// Products with a microscaled 4-bit weight, wide form: many tokens, where the
+// tensor cores and the way into them are the bound.
+//
+// A pair of CTAs (two SMs) computes a tile of 256 weight rows x up to 224
+// tokens with cta_group::2 MMAs: each CTA brings its own 128 rows of the
+// weight and half of the tokens, so that a byte in shared memory feeds twice
+// the products of a single CTA's tile. At the 4-bit rate a lone CTA would
+// have to write and read 192 bytes of shared memory a cycle, a pair 128.
+// Persistent: one pair for every two SMs walks over the tiles; two
+// accumulators of 224 columns let a tile's outputs be stored while the next
+// tile is computed (2 x 256 would leave no columns for the scales).
+//
+// Each CTA fills its own ring: warp 0 copies codes and weight scales (TMA),
+// warps 2 to 5 place all the tile's token scales (row-major in memory) in the
+// tensor core's order; both report to the first CTA's barriers, whose warp 1
+// issues scale copies to tensor memory and MMAs for the pair. Warps 6 to 9 are
+// the epilogue.
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp4.h"
+#include "fp4_device.cuh"
+#include "tc5.cuh"
+
+namespace mq {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kMaxStages = 8;
+constexpr int kBoxRows = 16;   // tokens of one copy in a tile that is not full
+constexpr int kATile = 128 * 128;
+constexpr int kMaxTT = 224;    // most tokens of a tile
+constexpr int kLoaders = 4, kLoadRows = (kMaxTT + 32 * kLoaders - 1) / (32 * kLoaders);
+
+struct WideParams {
+    CUtensorMap tw, tx, tx_small;  // boxes of 128 rows, TT / 2 tokens, 16 tokens
+    CUtensorMap tws;               // weight scales, one piece a box
+    const float *wfactor;
+    const uint8_t *xscales;
+    const float *xfactor;
+    const int32_t *offsets;
+    void *Y;
+    long long ldy, xspitch;
+    int *err;
+    long long N;
+    int NT;   // pairs of 128-row tiles
+    int NT1;  // 128-row tiles (of the weight scales)
+    int KS, E, R;
+    int TT;
+    int stages;
+    int fp16;
+    int paired;  // N, the stride and Y's address are even: 4-byte stores
+};
+
+template <bool NV>
+struct WideSmem {
+    static constexpr int kUnits = NV ? 4 : 2;
+    static constexpr int kTT = NV ? 192 : kMaxTT;  // columns of one accumulator
+    static constexpr uint32_t kScaleCols = 2 * kTT, kScaleSet = 12 * kUnits;
+    static constexpr int kA = kUnits * 512, kB = kUnits * 1024;  // scales: 128 rows, 256 tokens
+    __host__ __device__ static int slot(int TT) { return kATile + TT * 64 + kA + kB; }
+    __host__ __device__ static int total(int TT, int stages) { return slot(TT) * stages + 1024 + 256 + 4 * kMaxTT * 4; }
+};
+
+template <bool NV>
+__global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_constant__ WideParams p) {
+    using S = WideSmem<NV>;
+    constexpr int kUnits = S::kUnits;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int TT = p.TT, stages = p.stages, slot = S::slot(TT), KS = p.KS;
+    const int at_b = kATile, at_sa = kATile + TT * 64, at_sb = at_sa + S::kA;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + slot * stages);
+    uint64_t *full = bars, *empty = bars + kMaxStages, *acc_full = bars + 2 * kMaxStages, *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    const uint32_t rank = cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1 + 2 * kLoaders);  // the first CTA's producer, both CTAs' loaders
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8);  // the epilogue warps of both CTAs
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tc5::alloc<2>(tmem_slot, 512);
+    tc5::fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc5::fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    TileWalk walk(p.offsets, p.E, p.R, TT, p.NT);
+    Tile t;
+
+    if (warp == 0) {
+        int s = 0, ph = 1, first = 1;
+        bool ok = true;
+        for (long long ti = pair; ok && walk.find(ti, t); ti += pairs) {
+            const int n0 = (t.nt * 2 + rank) * 128;
+            const int n = (t.tokens + 31) / 32 * 32;  // the MMA's columns, unless the tile is full
+            const bool whole = n >= TT;
+            const int half = whole ? TT / 2 : n / 2;
+            const uint32_t bytes = 2 * (kATile + S::kA + half * 128);  // both CTAs' copies
+            // past the last row tile (an odd count) the codes read as zeros and the scales
+            // are another tile's: rows that are not stored
+            const int nt1 = min(t.nt * 2 + static_cast<int>(rank), p.NT1 - 1);
+            const int piece = (t.e * p.NT1 + nt1) * KS;
+            const int mb = t.m0 + rank * half;
+            auto weight = [&](int k, int slot_i) {
+                uint8_t *at = smem + slot_i * slot;
+                const uint32_t bar = in_cta(&full[slot_i], 0);
+                if (rank == 0) mbar_arrive_expect_tx(&full[slot_i], bytes);
+                tma_pair_load_3d(at, &p.tw, bar, k * 128, n0, t.e);
+                tma_pair_load_2d(at + at_sa, &p.tws, bar, 0, (piece + k) * (S::kA / 256));
+            };
+            auto tokens_in = [&](int k, int slot_i) {
+                uint8_t *at = smem + slot_i * slot + at_b;
+                const uint32_t bar = in_cta(&full[slot_i], 0);
+                if (whole)
+                    tma_pair_load_2d(at, &p.tx, bar, k * 128, mb);
+                else
+                    for (int b = 0; b < half; b += kBoxRows)
+                        tma_pair_load_2d(at + b * 128, &p.tx_small, bar, k * 128, mb + b);
+            };
+            int k = 0;
+            if (first) {
+                // the weight does not depend on the launch before: its first stages go ahead
+                const int ahead = min(stages, KS);
+                if (tc5::elect())
+                    for (int i = 0; i < ahead; ++i) weight(i, i);
+                __syncwarp();
+                pdl_wait();
+                if (tc5::elect())
+                    for (int i = 0; i < ahead; ++i) tokens_in(i, i);
+                __syncwarp();
+                k = ahead;
+                s = ahead == stages ? 0 : ahead;
+                if (ahead == stages) ph ^= 1;
+                first = 0;
+            }
+            for (; k < KS && ok; ++k) {
+                ok = mbar_wait(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (tc5::elect()) {
+                    weight(k, s);
+                    tokens_in(k, s);
+                }
+                __syncwarp();
+                if (++s == stages) s = 0, ph ^= 1;
+            }
+        }
+    } else if (warp == 1 && rank == 1) {
+        // the first CTA's warp 1 issues for both
+    } else if (warp == 1) {
+        int s = 0, ph = 0, b = 0, bph = 1, set = 0;
+        bool ok = true;
+        for (long long ti = pair; ok && walk.find(ti, t); ti += pairs) {
+            const int n = min(TT, (t.tokens + 31) / 32 * 32);
+            const uint32_t desc = tc5::idesc(256, n, !NV);
+            const uint32_t d = tmem + b * S::kTT;
+            ok = mbar_wait(&acc_empty[b], bph, p.err, kErrWaitEmpty, abort_flag);
+            for (int k = 0; k < KS && ok; ++k) {
+                ok = mbar_wait(&full[s], ph, p.err, kErrWaitFull, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc5::fence_after();
+                const uint32_t at = smem_u32(smem) + s * slot;
+                const uint32_t sa = at + at_sa, sb = at + at_sb;
+                const uint32_t sfa = tmem + S::kScaleCols + set * S::kScaleSet, sfb = sfa + 4 * kUnits;
+                const uint64_t da = tc5::operand_desc(at), db = tc5::operand_desc(at + at_b);
+                if (tc5::elect()) {
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) {
+                        tc5::copy_scales<2>(sfa + 4 * u, tc5::scale_desc(sa + 512 * u));
+                        tc5::copy_scales<2>(sfb + 8 * u, tc5::scale_desc(sb + 1024 * u));
+                        if (n > 128) tc5::copy_scales<2>(sfb + 8 * u + 4, tc5::scale_desc(sb + 1024 * u + 512));
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int u = NV ? q : q >> 1;
+                        const uint32_t byte = NV ? 0 : (q & 1) * 2;
+                        tc5::mma<2, NV>(d, da + 2 * q, db + 2 * q, desc | tc5::idesc_scale_byte(byte), sfa + 4 * u,
+                                        sfb + 8 * u, k > 0 || q > 0);
+                    }
+                    tc5::commit_pair(&empty[s]);
+                }
+                __syncwarp();
+                set ^= 1;
+                if (++s == stages) s = 0, ph ^= 1;
+            }
+            if (tc5::elect()) tc5::commit_pair(&acc_full[b]);
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            if (++b == 2) b = 0, bph ^= 1;
+        }
+    } else if (warp < 6) {
+        // the tokens' scales, two stages at a time: a row's 32 (MQ_FP4_MX: 16)
+        // bytes are read in one go, one pair of stages ahead of their turn
+        pdl_wait();
+        constexpr int kVec = NV ? 2 : 1;
+        uint4 next[kLoadRows][kVec];
+        const int t0 = threadIdx.x - 64;
+        auto read = [&](const Tile &tile, int k) {
+#pragma unroll
+            for (int i = 0; i < kLoadRows; ++i) {
+                const int r = t0 + i * 32 * kLoaders;
+                if (r < tile.tokens) {
+                    const uint8_t *src = p.xscales + (tile.m0 + r) * p.xspitch + static_cast<long long>(k) * (4 * kUnits);
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v)
+                        if (NV ? k + v < KS : true)
+                            asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(next[i][v].x), "=r"(next[i][v].y), "=r"(next[i][v].z),
+                                           "=r"(next[i][v].w)
+                                         : "l"(src + 16 * v));
+                }
+            }
+        };
+        int s = 0, ph = 1;
+        bool ok = true;
+        bool have = walk.find(pair, t);
+        if (have) read(t, 0);
+        for (long long ti = pair; have && ok;) {
+            const Tile cur = t;
+            ti += pairs;
+            have = walk.find(ti, t);
+            for (int k = 0; k < KS && ok; k += 2) {
+                uint4 now[kLoadRows][kVec];
+#pragma unroll
+                for (int i = 0; i < kLoadRows; ++i)
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v) now[i][v] = next[i][v];
+                if (k + 2 < KS)
+                    read(cur, k + 2);
+                else if (have)
+                    read(t, 0);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (k + j >= KS) break;
+                    ok = mbar_wait_warp(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag);
+                    if (!ok) break;
+                    uint8_t *at = smem + s * slot + at_sb;
+#pragma unroll
+                    for (int i = 0; i < kLoadRows; ++i) {
+                        const int r = t0 + i * 32 * kLoaders;
+                        if (r < cur.tokens) {
+                            uint32_t *dst = reinterpret_cast<uint32_t *>(at + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4);
+                            const uint4 v = now[i][NV ? j : 0];
+                            if constexpr (NV) {
+                                dst[0] = v.x;
+                                dst[256] = v.y;
+                                dst[512] = v.z;
+                                dst[768] = v.w;
+                            } else {
+                                dst[0] = j ? v.z : v.x;
+                                dst[256] = j ? v.w : v.y;
+                            }
+                        }
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(in_cta(&full[s], 0));
+                    if (++s == stages) s = 0, ph ^= 1;
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        // A warp stores 32 rows of the tile (its lanes) token by token. With
+        // even addresses two neighbouring lanes trade halves first, so that a
+        // store carries two rows of one token and a warp's store two tokens.
+        pdl_wait();
+        const int quad = warp & 3, row = quad * 32 + lane;
+        float *factors = reinterpret_cast<float *>(smem + slot * stages + 256) + quad * kMaxTT;
+        int b = 0, bph = 0;
+        for (long long ti = pair; walk.find(ti, t); ti += pairs) {
+            const long long n = (t.nt * 2 + static_cast<int>(rank)) * 128ll + row;
+            const bool live = n < p.N;
+            const float fw = NV && live ? __ldg(p.wfactor + static_cast<long long>(t.e) * p.N + n) : 1.0f;
+            if constexpr (NV) {
+                __syncwarp();
+                for (int m = lane; m < t.tokens; m += 32) factors[m] = p.xfactor[t.m0 + m];
+                __syncwarp();
+            }
+            if (!mbar_wait_warp(&acc_full[b], bph, p.err, kErrWaitMma, abort_flag)) break;
+            tc5::fence_after();
+            const uint32_t d = tmem + b * S::kTT + (static_cast<uint32_t>(quad) << 21);
+            uint32_t next[16];
+            tc5::load16(d, next);
+            for (int c = 0; c < t.tokens; c += 16) {
+                float v[16];
+                tc5::load_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(next[j]);
+                if (c + 16 < t.tokens) {
+                    tc5::load16(d + c + 16, next);
+                } else {
+                    // the accumulator is read: the next tile but one may use it
+                    tc5::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(in_cta(&acc_empty[b], 0));
+                }
+                if constexpr (NV) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(factors + c + j);
+                        v[j] = v[j] * f.x * fw;
+                        v[j + 1] = v[j + 1] * f.y * fw;
+                        v[j + 2] = v[j + 2] * f.z * fw;
+                        v[j + 3] = v[j + 3] * f.w * fw;
+                    }
+                }
+                const int left = t.tokens - c;
+                if (p.paired) {
+                    // even lanes store the chunk's even tokens, odd lanes its odd ones
+                    const int odd = lane & 1;
+                    uint32_t *y = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.Y) +
+                                                               (t.m0 + c + odd) * p.ldy + (n - odd));
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const uint32_t mine = p.fp16 ? pack_f16(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                        const uint32_t w = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+                        if (live && j + odd < left) *y = w;
+                        y += p.ldy;  // two rows of 16-bit values
+                    }
+                } else if (live) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < left) store_output(p.Y, (t.m0 + c + j) * p.ldy + n, v[j], p.fp16);
+                }
+            }
+            if (++b == 2) b = 0, bph ^= 1;
+        }
+    }
+    __syncwarp();
+    drain_after_abort(abort_flag);
+    __syncwarp();
+    tc5::fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still reach it
+    if (warp == 1) {
+        tc5::fence_after();
+        tc5::dealloc<2>(tmem, 512);
+    }
+}
+
+}  // namespace
+
+template <bool NV>
+static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,
+                          int64_t ldy, bool chained, cudaStream_t stream, int TT) {
+    using S = WideSmem<NV>;
+    WideParams p{};
+    p.TT = TT;
+    p.NT1 = static_cast<int>(d.NT);
+    p.NT = static_cast<int>((d.NT + 1) / 2);
+    // the most tiles that any split of the rows into matrices makes
+    const int64_t tiles = (offsets ? std::min<int64_t>(d.E, x.rows) + x.rows / TT : (x.rows + TT - 1) / TT) * p.NT;
+    p.stages = std::min(kMaxStages, (227 * 1024 - S::total(TT, 0)) / S::slot(TT));
+    p.tw = d.map;
+    if (!encode_bytes_map(&p.tx, x.codes, d.pitch, x.rows, 0, TT / 2) ||
+        !encode_bytes_map(&p.tx_small, x.codes, d.pitch, x.rows, 0, kBoxRows))
+        return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activations");
+    p.tws = d.scale_map;
+    p.paired = d.N % 2 == 0 && ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(Y) & 3) == 0;
+    p.wfactor = d.row_scale;
+    p.xscales = x.scales;
+    p.xfactor = x.row_scale;
+    p.offsets = offsets;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.xspitch = fp4_scale_pitch(d.fmt, d.K);
+    p.err = d.err;
+    p.N = d.N;
+    p.KS = d.KS;
+    p.E = static_cast<int>(d.E);
+    p.R = static_cast<int>(x.rows);
+    p.fp16 = dtype == MQ_FP16;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(MQ_ERR_CUDA, "cudaGetDevice failed");
+    if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
+    static bool configured[64] = {};
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(fp4_wide_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+            cudaSuccess)
+            return fail(MQ_ERR_CUDA, "fp4 linear: device setup failed");
+        configured[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, sm_count() / 2)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::total(TT, p.stages);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = chained ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_wide_kernel<NV>, p);
+    if (e != cudaSuccess) return fail(MQ_ERR_CUDA, std::string("fp4 linear launch: ") + cudaGetErrorString(e));
+    return MQ_OK;
+}
+
+mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,
+                          int64_t ldy, bool chained, cudaStream_t stream) {
+    // Tokens of a tile: the choice that leaves the least time over the waves
+    // of tiles, a tile's time growing with its tokens plus a share that does
+    // not depend on them.
+    const int64_t NT = (d.NT + 1) / 2, pairs = sm_count() / 2;
+    const int most = d.fmt == MQ_FP4_NV ? WideSmem<true>::kTT : WideSmem<false>::kTT;
+    int best = most;
+    if (!offsets) {
+        int64_t least = -1;
+        for (int TT = most; TT >= 64; TT -= 32) {
+            const int64_t tiles = (x.rows + TT - 1) / TT * NT;
+            const int64_t cost = (tiles + pairs - 1) / pairs * (TT + 64);
+            if (least < 0 || cost < least) least = cost, best = TT;
+        }
+    }
+    return d.fmt == MQ_FP4_NV ? run_wide<true>(d, x, offsets, Y, dtype, ldy, chained, stream, best)
+                              : run_wide<false>(d, x, offsets, Y, dtype, ldy, chained, stream, best);
+}
+
+}  // namespace mq

@@ -38,6 +38,16 @@ __device__ __forceinline__ void fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// One lane of a converged warp. The instructions below take their operands
+// from registers that a warp shares: a loop that the whole warp runs, with
+// their issue alone under elect(), lets the compiler keep descriptors and
+// addresses there.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Shared-memory matrix descriptors (version 1). Operands: K-major rows of 128
 // bytes, 128-byte swizzle, groups of 8 rows 1024 bytes apart. Scales: units of
 // 32 rows x 16 bytes, no swizzle, groups of 8 rows 128 bytes apart.
@@ -107,18 +117,16 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
         : "memory");
 }
 
-// 32 lanes x 16 columns of 32-bit values: thread i gets lane (base + i).
-__device__ __forceinline__ void load16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
+// 32 lanes x 16 columns of 32-bit values: thread i gets lane (base + i). The
+// values are there after load_wait.
+__device__ __forceinline__ void load16(uint32_t taddr, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 }  // namespace tc5
 }  // namespace mq

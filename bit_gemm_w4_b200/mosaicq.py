@@ -448,25 +448,52 @@ class Weight:
 
 
 # ---------------------------------------------------------------- fp4
-# Microscaled 4-bit floating point (mq_fp4_*).
+# Microscaled 4-bit floating point (mq_fp4_*). A single token's product takes
+# a few microseconds on the device, so the way there is kept short: a call on
+# the tensors' own device and its current stream enters no context.
 
-_DTYPES = {}  # torch dtype -> mq_dtype, filled when torch is first needed
+class _Lazy:
+    """torch and what the calls need of it, imported when first used."""
+
+    def __getattr__(self, name):
+        import torch
+        self.torch = torch
+        self.empty = torch.empty
+        self.bf16, self.fp32, self.u8 = torch.bfloat16, torch.float32, torch.uint8
+        self.dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # mq_dtype
+        self.current_device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        return self.__dict__[name]
+
+
+_t = _Lazy()
 
 
 def _dtype(t, where: str, fp32: bool = False) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    d = _DTYPES.get(t)
+    d = _t.dtypes.get(t)
     if d is None or (d == 2 and not fp32):
         raise ValueError(f"{where}: unsupported dtype {t}")
     return d
 
 
 def _fmt(fmt) -> int:
-    if fmt not in FP4_FORMATS:
+    f = FP4_FORMATS.get(fmt)
+    if f is None:
         raise ValueError(f"fp4 format must be one of {sorted(FP4_FORMATS)}, not {fmt!r}")
-    return FP4_FORMATS[fmt]
+    return f
+
+
+def _cuda_index(t) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"a CUDA tensor is needed, not one on {t.device}")
+    return index
+
+
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or _t.current_device() != index
 
 
 class _On:
@@ -474,49 +501,44 @@ class _On:
     current while it runs, so that what the call allocates and converts
     belongs to that stream too."""
 
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"a CUDA tensor is needed, not one on {device}")
-        self.cuda, self.device, self.given = torch.cuda, device, stream
+    def __init__(self, index: int, stream):
+        self.index, self.given = index, stream
 
     def __enter__(self):
-        cuda = self.cuda
+        cuda = _t.torch.cuda
         self.prev = cuda.current_device()
-        self.index = self.prev if self.device.index is None else self.device.index
         if self.index != self.prev:
             cuda.set_device(self.index)
         self.was = None
-        current = cuda.current_stream()
-        self.stream = current.cuda_stream
-        if self.given is not None and _stream(self.given) != self.stream:
-            self.stream = _stream(self.given)
-            self.was = current
-            cuda.set_stream(self.given if isinstance(self.given, cuda.Stream) else
-                            cuda.ExternalStream(self.stream) if self.stream else cuda.default_stream())
-        return self
+        if self.given is not None:
+            current, ptr = cuda.current_stream(), _stream(self.given)
+            if ptr != current.cuda_stream:
+                self.was = current
+                cuda.set_stream(self.given if isinstance(self.given, cuda.Stream) else
+                                cuda.ExternalStream(ptr) if ptr else cuda.default_stream())
 
     def __exit__(self, *exc):
         if self.was is not None:
-            self.cuda.set_stream(self.was)
+            _t.torch.cuda.set_stream(self.was)
         if self.index != self.prev:
-            self.cuda.set_device(self.prev)
+            _t.torch.cuda.set_device(self.prev)
 
 
 def _rows_view(X, where: str):
-    """A [rows, K] tensor whose rows are contiguous, and its row stride."""
+    """A 2-D tensor whose rows are contiguous, its sizes and row stride."""
     if X.dim() != 2 or X.shape[1] < 1:
         raise ValueError(f"{where}: a 2-D tensor with at least one column is needed")
     M, K = X.shape
-    if (X.stride(1) != 1 and K > 1) or (X.stride(0) < K and M > 1):
-        X = X.contiguous()
-    return X, (X.stride(0) if M > 1 else K)
+    ld, one = X.stride()
+    if (one != 1 and K > 1) or (ld < K and M > 1):
+        X, ld = X.contiguous(), K
+    return X, M, K, (ld if M > 1 else K)
 
 
-def _index(t, device, where: str):
-    import torch
-    if t.device != device or t.dim() != 1 or t.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"{where} must be a 1-D int32 or int64 tensor on {device}")
+def _index(t, index: int, where: str):
+    torch = _t.torch
+    if t.get_device() != index or t.dim() != 1 or t.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"{where} must be a 1-D int32 or int64 tensor on cuda:{index}")
     if t.dtype == torch.int64:  # what int32 cannot hold is out of range either way
         t = t.clamp(-1, 2**31 - 1).to(torch.int32)
     return t.contiguous()
@@ -529,20 +551,19 @@ class Fp4Tensor:
     __slots__ = ("codes", "scales", "row_scale", "K", "fmt")
 
     def __init__(self, codes, scales, row_scale, K: int, fmt: str):
-        import torch
         f = _fmt(fmt)
         K = int(K)
         want = (_lib.mq_fp4_code_bytes(K), _lib.mq_fp4_scale_bytes(f, K))
         if not want[0]:
             raise ValueError("K must be in [1, 2^24]")
         for t, name, width in ((codes, "codes", want[0]), (scales, "scales", want[1])):
-            if t.dtype != torch.uint8 or t.dim() < 2 or t.shape[-1] != width or not t.is_contiguous():
+            if t.dtype != _t.u8 or t.dim() < 2 or t.shape[-1] != width or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous uint8 [..., {width}] tensor")
         if codes.shape[:-1] != scales.shape[:-1] or codes.device != scales.device:
             raise ValueError("codes and scales must have the same rows and device")
         if (row_scale is None) != (fmt == "mxfp4"):
             raise ValueError("row_scale belongs to nvfp4, and only to it")
-        if row_scale is not None and (row_scale.dtype != torch.float32 or row_scale.shape != codes.shape[:-1] or
+        if row_scale is not None and (row_scale.dtype != _t.fp32 or row_scale.shape != codes.shape[:-1] or
                                       not row_scale.is_contiguous() or row_scale.device != codes.device):
             raise ValueError("row_scale must be a contiguous float32 tensor, one value for each row")
         self.codes, self.scales, self.row_scale, self.K, self.fmt = codes, scales, row_scale, K, fmt
@@ -553,12 +574,13 @@ class Fp4Tensor:
 
     @classmethod
     def empty(cls, rows: int, K: int, fmt: str, device) -> "Fp4Tensor":
-        import torch
+        """Room for a quantised [rows, K] matrix."""
         f = _fmt(fmt)
         q = cls.__new__(cls)
-        q.codes = torch.empty((rows, _lib.mq_fp4_code_bytes(K)), dtype=torch.uint8, device=device)
-        q.scales = torch.empty((rows, _lib.mq_fp4_scale_bytes(f, K)), dtype=torch.uint8, device=device)
-        q.row_scale = torch.empty(rows, dtype=torch.float32, device=device) if f else None
+        empty, u8 = _t.empty, _t.u8
+        q.codes = empty((rows, _lib.mq_fp4_code_bytes(K)), dtype=u8, device=device)
+        q.scales = empty((rows, _lib.mq_fp4_scale_bytes(f, K)), dtype=u8, device=device)
+        q.row_scale = empty(rows, dtype=_t.fp32, device=device) if f else None
         q.K, q.fmt = K, fmt
         return q
 
@@ -568,12 +590,18 @@ class Fp4Tensor:
 
     def dequantize(self, dtype=None, *, stream=None):
         """The values as a [rows, K] tensor (fp32 unless a dtype is given)."""
-        import torch
-        d = _dtype(torch.float32 if dtype is None else dtype, "dequantize", fp32=True)
-        with _On(self.codes.device, stream) as on:
-            Y = torch.empty((self.rows, self.K), dtype=dtype or torch.float32, device=self.codes.device)
-            _check(_lib.mq_fp4_dequantize(*self._ptrs(), self.rows, self.K, FP4_FORMATS[self.fmt], Y.data_ptr(), d,
-                                          self.K, on.stream), "mq_fp4_dequantize")
+        index = _cuda_index(self.codes)
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return self.dequantize(dtype)
+        dtype = _t.fp32 if dtype is None else dtype
+        d = _dtype(dtype, "dequantize", fp32=True)
+        rows, K = self.rows, self.K
+        Y = _t.empty((rows, K), dtype=dtype, device=self.codes.device)
+        st = _lib.mq_fp4_dequantize(*self._ptrs(), rows, K, FP4_FORMATS[self.fmt], Y.data_ptr(), d, K,
+                                    _t.raw_stream(index))
+        if st:
+            _check(st, "mq_fp4_dequantize")
         return Y
 
 
@@ -583,14 +611,19 @@ def fp4_quantize(X, fmt: str = "nvfp4", *, rows=None, stream=None) -> Fp4Tensor:
     and zeros where rows[r] is no row of X."""
     f = _fmt(fmt)
     d = _dtype(X.dtype, "fp4_quantize", fp32=True)
-    with _On(X.device, stream) as on:
-        X, ldx = _rows_view(X, "fp4_quantize")
-        if rows is not None:
-            rows = _index(rows, X.device, "rows")
-        M = X.shape[0] if rows is None else rows.shape[0]
-        q = Fp4Tensor.empty(M, X.shape[1], fmt, X.device)
-        _check(_lib.mq_fp4_quantize(X.data_ptr(), d, M, X.shape[1], ldx, None if rows is None else rows.data_ptr(),
-                                    X.shape[0], f, *q._ptrs(), on.stream), "mq_fp4_quantize")
+    index = _cuda_index(X)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return fp4_quantize(X, fmt, rows=rows)
+    X, M, K, ldx = _rows_view(X, "fp4_quantize")
+    R, at = M, None
+    if rows is not None:
+        rows = _index(rows, index, "rows")
+        R, at = rows.shape[0], rows.data_ptr()
+    q = Fp4Tensor.empty(R, K, fmt, X.device)
+    st = _lib.mq_fp4_quantize(X.data_ptr(), d, R, K, ldx, at, M, f, *q._ptrs(), _t.raw_stream(index))
+    if st:
+        _check(st, "mq_fp4_quantize")
     return q
 
 
@@ -599,13 +632,13 @@ class Fp4Weight:
     (owns its device buffers): a linear layer (E = 1) or a layer's experts."""
 
     def __init__(self, handle: int):
-        import torch
         self._h = handle
         i = _Fp4Info()
         _check(_lib.mq_fp4_get_info(handle, ctypes.byref(i)), "mq_fp4_get_info")
         self.E, self.N, self.K, self.device_bytes = i.E, i.N, i.K, i.device_bytes
         self.fmt = {v: k for k, v in FP4_FORMATS.items()}[i.format]
-        self.device = torch.device("cuda", i.device)
+        self._index = i.device
+        self.device = _t.torch.device("cuda", i.device)
 
     @classmethod
     def pack(cls, W, fmt: str = "nvfp4", *, stream=None) -> "Fp4Weight":
@@ -615,12 +648,15 @@ class Fp4Weight:
         d = _dtype(W.dtype, "Fp4Weight.pack", fp32=True)
         if W.dim() not in (2, 3):
             raise ValueError("W must be [N, K] or [E, N, K]")
+        index = _cuda_index(W)
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return cls.pack(W, fmt)
         h = ctypes.c_void_p()
-        with _On(W.device, stream) as on:
-            W = W.contiguous()
-            E = W.shape[0] if W.dim() == 3 else 1
-            _check(_lib.mq_fp4_pack(W.data_ptr(), d, E, W.shape[-2], W.shape[-1], f, on.stream, ctypes.byref(h)),
-                   "mq_fp4_pack")
+        W = W.contiguous()
+        E = W.shape[0] if W.dim() == 3 else 1
+        _check(_lib.mq_fp4_pack(W.data_ptr(), d, E, W.shape[-2], W.shape[-1], f, _t.raw_stream(index),
+                                ctypes.byref(h)), "mq_fp4_pack")
         return cls(h.value)
 
     @classmethod
@@ -630,11 +666,14 @@ class Fp4Weight:
         q = Fp4Tensor(codes, scales, row_scale, K, fmt)
         if codes.dim() not in (2, 3):
             raise ValueError("codes must be [N, .] or [E, N, .]")
+        index = _cuda_index(codes)
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return cls.pack_codes(codes, scales, row_scale, K, fmt)
         h = ctypes.c_void_p()
-        with _On(codes.device, stream) as on:
-            E = codes.shape[0] if codes.dim() == 3 else 1
-            _check(_lib.mq_fp4_pack_codes(*q._ptrs(), E, codes.shape[-2], q.K, FP4_FORMATS[fmt], on.stream,
-                                          ctypes.byref(h)), "mq_fp4_pack_codes")
+        E = codes.shape[0] if codes.dim() == 3 else 1
+        _check(_lib.mq_fp4_pack_codes(*q._ptrs(), E, codes.shape[-2], q.K, FP4_FORMATS[fmt], _t.raw_stream(index),
+                                      ctypes.byref(h)), "mq_fp4_pack_codes")
         return cls(h.value)
 
     @property
@@ -646,53 +685,65 @@ class Fp4Weight:
 
     def export(self, *, stream=None) -> Fp4Tensor:
         """The packed matrices as one quantised [E * N, K] matrix."""
-        with _On(self.device, stream) as on:
-            q = Fp4Tensor.empty(self.E * self.N, self.K, self.fmt, self.device)
-            _check(_lib.mq_fp4_export(self._h, *q._ptrs(), on.stream), "mq_fp4_export")
+        if _elsewhere(self._index, stream):
+            with _On(self._index, stream):
+                return self.export()
+        q = Fp4Tensor.empty(self.E * self.N, self.K, self.fmt, self.device)
+        _check(_lib.mq_fp4_export(self._h, *q._ptrs(), _t.raw_stream(self._index)), "mq_fp4_export")
         return q
 
     def _output(self, Y, rows: int, dtype):
-        import torch
         if Y is None:
-            Y = torch.empty((rows, self.N), dtype=dtype, device=self.device)
-        elif Y.device != self.device or Y.dtype != dtype or Y.shape != (rows, self.N) or \
+            return _t.empty((rows, self.N), dtype=dtype, device=self.device), self.N
+        if Y.device != self.device or Y.dtype != dtype or Y.shape != (rows, self.N) or \
                 (Y.stride(1) != 1 and self.N > 1) or (Y.stride(0) < self.N and rows > 1):
             raise ValueError(f"Y must be a {dtype} [{rows}, {self.N}] tensor on {self.device} with contiguous rows")
         return Y, (Y.stride(0) if rows > 1 else self.N)
 
     def _workspace(self, workspace, rows: int):
-        import torch
         if workspace is None:
-            workspace = torch.empty(max(16, self.workspace_bytes(rows)), dtype=torch.uint8, device=self.device)
-        elif workspace.device != self.device or not workspace.is_contiguous():
+            n = _lib.mq_fp4_workspace_bytes(self._h, rows)
+            return _t.empty(n, dtype=_t.u8, device=self.device), n
+        if workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
-        return workspace
+        return workspace, workspace.numel() * workspace.element_size()
 
     def _quantized(self, X: Fp4Tensor, dtype):
-        import torch
-        if X.fmt != self.fmt or X.K != self.K or X.codes.device != self.device:
+        if X.fmt != self.fmt or X.K != self.K or X.codes.get_device() != self._index:
             raise ValueError(f"the activations must be {self.fmt} with K = {self.K} on {self.device}")
-        dtype = torch.bfloat16 if dtype is None else dtype
+        dtype = _t.bf16 if dtype is None else dtype
         return dtype, _dtype(dtype, "the output")
+
+    def _input(self, X, dtype):
+        d = _dtype(X.dtype, "X")
+        if dtype is not None and dtype != X.dtype:
+            raise ValueError("Y has the type of X; dtype is for quantised activations")
+        if X.get_device() != self._index or X.dim() != 2 or X.shape[1] != self.K:
+            raise ValueError(f"X must be a [rows, {self.K}] tensor on {self.device}")
+        return d, *_rows_view(X, "X")
 
     def linear(self, X, Y=None, workspace=None, *, dtype=None, stream=None):
         """Y = X @ W^T. X: a bf16 or fp16 [M, K] tensor, quantised within the
         call into the workspace (workspace_bytes(M) bytes), with Y of its
         type; or an Fp4Tensor, with Y of `dtype` (bf16 unless given)."""
+        index = self._index
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return self.linear(X, Y, workspace, dtype=dtype)
         if isinstance(X, Fp4Tensor):
             dtype, d = self._quantized(X, dtype)
-            with _On(self.device, stream) as on:
-                Y, ldy = self._output(Y, X.rows, dtype)
-                _check(_lib.mq_fp4_linear_codes(self._h, *X._ptrs(), X.rows, Y.data_ptr(), d, ldy, on.stream),
-                       "mq_fp4_linear_codes")
+            Y, ldy = self._output(Y, X.rows, dtype)
+            st = _lib.mq_fp4_linear_codes(self._h, *X._ptrs(), X.rows, Y.data_ptr(), d, ldy, _t.raw_stream(index))
+            if st:
+                _check(st, "mq_fp4_linear_codes")
             return Y
-        with _On(self.device, stream) as on:
-            X, d, ldx = self._input(X, dtype)
-            M = X.shape[0]
-            Y, ldy = self._output(Y, M, X.dtype)
-            workspace = self._workspace(workspace, M)
-            _check(_lib.mq_fp4_linear(self._h, X.data_ptr(), d, M, ldx, Y.data_ptr(), ldy, workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), on.stream), "mq_fp4_linear")
+        d, X, M, _, ldx = self._input(X, dtype)
+        Y, ldy = self._output(Y, M, X.dtype)
+        workspace, nbytes = self._workspace(workspace, M)
+        st = _lib.mq_fp4_linear(self._h, X.data_ptr(), d, M, ldx, Y.data_ptr(), ldy, workspace.data_ptr(), nbytes,
+                                _t.raw_stream(index))
+        if st:
+            _check(st, "mq_fp4_linear")
         return Y
 
     def linear_grouped(self, X, offsets, Y=None, workspace=None, *, rows=None, dtype=None, stream=None):
@@ -701,47 +752,42 @@ class Fp4Weight:
         X[rows[r]], or X[r] without rows; X as for linear. Rows of Y that
         belong to no expert are left as they were (undefined in a Y that the
         call makes)."""
-        if offsets.dim() != 1 or offsets.shape[0] != self.E + 1:
+        index = self._index
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return self.linear_grouped(X, offsets, Y, workspace, rows=rows, dtype=dtype)
+        offsets = _index(offsets, index, "offsets")
+        if offsets.shape[0] != self.E + 1:
             raise ValueError(f"offsets must hold E + 1 = {self.E + 1} values")
         if isinstance(X, Fp4Tensor):
             if rows is not None:
                 raise ValueError("rows are taken when X is quantised: fp4_quantize(X, rows=rows)")
             dtype, d = self._quantized(X, dtype)
-            with _On(self.device, stream) as on:
-                offsets = _index(offsets, self.device, "offsets")
-                Y, ldy = self._output(Y, X.rows, dtype)
-                _check(_lib.mq_fp4_linear_grouped_codes(self._h, *X._ptrs(), X.rows, offsets.data_ptr(),
-                                                        Y.data_ptr(), d, ldy, on.stream),
-                       "mq_fp4_linear_grouped_codes")
+            Y, ldy = self._output(Y, X.rows, dtype)
+            st = _lib.mq_fp4_linear_grouped_codes(self._h, *X._ptrs(), X.rows, offsets.data_ptr(), Y.data_ptr(), d,
+                                                  ldy, _t.raw_stream(index))
+            if st:
+                _check(st, "mq_fp4_linear_grouped_codes")
             return Y
-        with _On(self.device, stream) as on:
-            X, d, ldx = self._input(X, dtype)
-            offsets = _index(offsets, self.device, "offsets")
-            if rows is not None:
-                rows = _index(rows, self.device, "rows")
-            R = X.shape[0] if rows is None else rows.shape[0]
-            Y, ldy = self._output(Y, R, X.dtype)
-            workspace = self._workspace(workspace, R)
-            _check(_lib.mq_fp4_linear_grouped(self._h, X.data_ptr(), d, X.shape[0], ldx,
-                                              None if rows is None else rows.data_ptr(), R, offsets.data_ptr(),
-                                              Y.data_ptr(), ldy, workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size(), on.stream),
-                   "mq_fp4_linear_grouped")
+        d, X, M, _, ldx = self._input(X, dtype)
+        R, at = M, None
+        if rows is not None:
+            rows = _index(rows, index, "rows")
+            R, at = rows.shape[0], rows.data_ptr()
+        Y, ldy = self._output(Y, R, X.dtype)
+        workspace, nbytes = self._workspace(workspace, R)
+        st = _lib.mq_fp4_linear_grouped(self._h, X.data_ptr(), d, M, ldx, at, R, offsets.data_ptr(), Y.data_ptr(), ldy,
+                                        workspace.data_ptr(), nbytes, _t.raw_stream(index))
+        if st:
+            _check(st, "mq_fp4_linear_grouped")
         return Y
 
-    def _input(self, X, dtype):
-        if dtype is not None and dtype != X.dtype:
-            raise ValueError("Y has the type of X; dtype is for quantised activations")
-        d = _dtype(X.dtype, "X")
-        if X.device != self.device or X.dim() != 2 or X.shape[1] != self.K:
-            raise ValueError(f"X must be a [rows, {self.K}] tensor on {self.device}")
-        X, ldx = _rows_view(X, "X")
-        return X, d, ldx
-
     def device_error(self, stream=None) -> int:
+        if _elsewhere(self._index, stream):
+            with _On(self._index, stream):
+                return self.device_error()
         code = ctypes.c_int32()
-        with _On(self.device, stream) as on:
-            st = _lib.mq_fp4_device_error(self._h, on.stream, ctypes.byref(code))
+        st = _lib.mq_fp4_device_error(self._h, _t.raw_stream(self._index), ctypes.byref(code))
         if st not in (OK, DEVICE_TIMEOUT):
             _check(st, "mq_fp4_device_error")
         return code.value
