@@ -409,32 +409,16 @@ bool encode_codes_map(CUtensorMap *map, const void *codes, int64_t M, int64_t K,
     return r == CUDA_SUCCESS;
 }
 
-bool encode_bytes_map(CUtensorMap *map, const void *base, int64_t pitch, int64_t rows, int64_t outer,
-                      int box_rows) {
+bool encode_bytes_map(CUtensorMap *map, const void *base, int64_t pitch, int64_t rows, int box_rows, bool swizzle) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(rows),
-                          static_cast<cuuint64_t>(outer)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(pitch) * rows};
-    cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    // a matrix alone is two-dimensional: its loads name no third coordinate
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, outer > 0 ? 3 : 2, const_cast<void *>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-bool encode_pieces_map(CUtensorMap *map, const void *base, int64_t bytes, int box_bytes) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(bytes / 256)};
-    cuuint64_t strides[1] = {256};
-    cuuint32_t box[2] = {256, static_cast<cuuint32_t>(box_bytes / 256)};
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 

@@ -34,27 +34,30 @@ struct Fp4Rows {
     int64_t rows;
 };
 
-// Device side of a packed weight: E matrices [N][K] of one format.
+// Device side of a packed weight: E matrices [N][K] of one format. A matrix is
+// held in pieces of 128 rows x one K stage, in the order the products read
+// them, [E][NT][KS]: a piece is what a CTA copies to shared memory in one go,
+// byte for byte as the tensor core takes it from there (a row-major matrix
+// would be read in 128-byte bits of 128 rows, which costs HBM a third of its
+// rate). Rows and columns past N and K are zeros.
+//   codes   16 KB: row r's 16-byte unit u at r * 128 + (u ^ r % 8) * 16 (the
+//           128-byte swizzle)
+//   scales  512-byte units of four scale columns: row r's column c at
+//           (c / 4) * 512 + (r % 32) * 16 + (r / 32) * 4 + c % 4
 struct Fp4Device {
     int64_t E = 0, N = 0, K = 0;
     int fmt = 0;
-    int64_t pitch = 0;  // bytes of a row of codes
-    int KS = 0;         // K stages
-    int64_t NT = 0;     // 128-row tiles of one matrix
-    // codes [E][N][pitch]
-    uint8_t *codes = nullptr;
-    // scales in the order the tensor core takes them: [E][NT][KS] pieces of
-    // 128 rows x one stage, each a run of 512-byte units of four scale
-    // columns; byte (row % 32) * 16 + (row / 32) * 4 + column % 4 of a unit
-    uint8_t *scales = nullptr;
+    int KS = 0;      // K stages
+    int64_t NT = 0;  // 128-row tiles of one matrix
+    uint8_t *pieces = nullptr;
     float *row_scale = nullptr;  // [E][N], NULL for MQ_FP4_MX
     int *err = nullptr;
-    CUtensorMap map;        // codes as [E][N][pitch] bytes, boxes of 128 rows x 128 bytes
-    CUtensorMap scale_map;  // scales as rows of 256 bytes, boxes of one piece
+    CUtensorMap map;  // pieces as rows of 128 bytes, a piece a box
 };
 
-// Bytes of one piece of `scales` above.
-constexpr int fp4_piece_bytes(int fmt) { return 128 * fp4_stage_scales(fmt); }
+constexpr int kFp4CodePiece = 128 * 128;
+constexpr int fp4_scale_piece(int fmt) { return 128 * fp4_stage_scales(fmt); }
+constexpr int fp4_piece(int fmt) { return kFp4CodePiece + fp4_scale_piece(fmt); }
 
 // X (dtype, row stride ldx elements) to codes, scales and (MQ_FP4_NV) row
 // factors, `rows` output rows; output row r is X row index[r] (index NULL: r),
@@ -66,9 +69,8 @@ mq_status launch_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64
 mq_status launch_fp4_dequantize(const Fp4Rows &x, int64_t K, int fmt, void *Y, mq_dtype dtype,
                                 int64_t ldy, cudaStream_t stream);
 
-// Row-major scales [E][N][scale pitch] to the order of Fp4Device::scales, or back.
-mq_status launch_fp4_scale_order(const Fp4Device &d, uint8_t *row_major, bool to_row_major,
-                                 cudaStream_t stream);
+// Row-major codes and scales ([E * N] rows) to a weight's pieces, or back.
+mq_status launch_fp4_order(const Fp4Device &d, uint8_t *codes, uint8_t *scales, bool to_rows, cudaStream_t stream);
 
 // Y[r] = x[r] * W[e]^T for the rows offsets[e] <= r < offsets[e + 1] of every
 // e (offsets NULL: E is 1 and every row belongs to it). `chained`: x was
@@ -77,18 +79,19 @@ mq_status launch_fp4_scale_order(const Fp4Device &d, uint8_t *row_major, bool to
 mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                             mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
 
+// The same from X as it is (as for launch_fp4_quantize), quantised by the
+// product itself, where fp4_linear_quantises says that this is the faster way.
+bool fp4_linear_quantises(const Fp4Device &d, int64_t rows);
+mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype dtype, int64_t rows, int64_t ldx,
+                                   const int32_t *index, int64_t x_rows, const int32_t *offsets, void *Y,
+                                   int64_t ldy, cudaStream_t stream);
+
 // The form of launch_fp4_linear for many tokens (fp4_wide.cu).
 mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                           mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
 
-// Byte matrix [outer][rows][pitch] (outer = 0: [rows][pitch], two coordinates)
-// as a tensor map with boxes of box_rows x 128 bytes, 128-byte swizzle, zero
-// fill.
-bool encode_bytes_map(CUtensorMap *map, const void *base, int64_t pitch, int64_t rows, int64_t outer,
-                      int box_rows);
-
-// `bytes` (a multiple of 256) as a tensor map of rows of 256 bytes with boxes
-// of box_bytes, in their order in memory.
-bool encode_pieces_map(CUtensorMap *map, const void *base, int64_t bytes, int box_bytes);
+// Rows of `pitch` bytes as a tensor map with boxes of box_rows x 128 bytes
+// (zeros past the end), with or without the 128-byte swizzle.
+bool encode_bytes_map(CUtensorMap *map, const void *base, int64_t pitch, int64_t rows, int box_rows, bool swizzle);
 
 }  // namespace mq

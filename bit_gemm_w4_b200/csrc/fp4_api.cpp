@@ -76,15 +76,13 @@ mq_status check_shape_fp4(int64_t E, int64_t N, int64_t K, int fmt) {
     return MQ_OK;
 }
 
-// The weight's device buffers; codes and row factors are copied from (or, with
-// NULL sources, left for the caller to write), scales left unwritten.
+// The weight's device buffers, left unwritten.
 mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
     Fp4Device &d = w->d;
     d.E = E;
     d.N = N;
     d.K = K;
     d.fmt = fmt;
-    d.pitch = fp4_code_pitch(K);
     d.KS = static_cast<int>((K + kFp4StageK - 1) / kFp4StageK);
     d.NT = (N + 127) / 128;
     auto get = [&](void **p, int64_t bytes) {
@@ -94,13 +92,12 @@ mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
         w->device_bytes += bytes;
         return MQ_OK;
     };
-    if (mq_status st = get(reinterpret_cast<void **>(&d.codes), E * N * d.pitch)) return st;
-    if (mq_status st = get(reinterpret_cast<void **>(&d.scales), E * d.NT * d.KS * fp4_piece_bytes(fmt))) return st;
+    const int64_t bytes = E * d.NT * d.KS * fp4_piece(fmt);
+    if (mq_status st = get(reinterpret_cast<void **>(&d.pieces), bytes)) return st;
     if (fmt == MQ_FP4_NV)
         if (mq_status st = get(reinterpret_cast<void **>(&d.row_scale), E * N * 4)) return st;
     if (mq_status st = get(reinterpret_cast<void **>(&d.err), 4)) return st;
-    if (!encode_bytes_map(&d.map, d.codes, d.pitch, N, E, 128) ||
-        !encode_pieces_map(&d.scale_map, d.scales, E * d.NT * d.KS * fp4_piece_bytes(fmt), fp4_piece_bytes(fmt)))
+    if (!encode_bytes_map(&d.map, d.pieces, 128, bytes / 128, fp4_piece(fmt) / 128, false))
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the weight");
     return MQ_OK;
 }
@@ -150,6 +147,11 @@ mq_status quantize_and_multiply(const mq_fp4_weight *w, const void *X, int dtype
     if (mq_status st = check_input(X, dtype, R, d.K, ldx, index, x_rows)) return st;
     if (R == 0) return MQ_OK;
     if (mq_status st = check_output(w, Y, dtype, ldy)) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (fp4_linear_quantises(d, R)) {
+        if (mq_status st = check_device(w)) return st;
+        return launch_fp4_linear_direct(d, X, static_cast<mq_dtype>(dtype), R, ldx, index, x_rows, offsets, Y, ldy, s);
+    }
     const Workspace ws(R, d.K, d.fmt);
     if (!workspace || !aligned16(workspace)) return fail(MQ_ERR_INVALID_ARG, "the workspace is NULL or not 16-byte aligned");
     if (workspace_bytes < static_cast<size_t>(ws.total))
@@ -157,7 +159,6 @@ mq_status quantize_and_multiply(const mq_fp4_weight *w, const void *X, int dtype
     if (mq_status st = check_device(w)) return st;
     uint8_t *base = static_cast<uint8_t *>(workspace);
     float *factors = d.fmt == MQ_FP4_NV ? reinterpret_cast<float *>(base + ws.factors) : nullptr;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (mq_status st = launch_fp4_quantize(X, static_cast<mq_dtype>(dtype), R, d.K, ldx, index, x_rows, d.fmt, base,
                                            base + ws.scales, factors, s))
         return st;
@@ -251,13 +252,14 @@ mq_status mq_fp4_pack_codes(const void *codes, const void *scales, const float *
     cudaError_t e = cudaSuccess;
     if (!st) {
         const Fp4Device &d = w->d;
-        e = cudaMemcpyAsync(d.codes, codes, E * N * d.pitch, cudaMemcpyDeviceToDevice, s);
-        if (e == cudaSuccess && d.row_scale)
+        if (d.row_scale)
             e = cudaMemcpyAsync(d.row_scale, row_scale, E * N * 4, cudaMemcpyDeviceToDevice, s);
         if (e == cudaSuccess) e = cudaMemsetAsync(d.err, 0, 4, s);
         if (e != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack_codes");
     }
-    if (!st) st = launch_fp4_scale_order(w->d, static_cast<uint8_t *>(const_cast<void *>(scales)), false, s);
+    if (!st)
+        st = launch_fp4_order(w->d, static_cast<uint8_t *>(const_cast<void *>(codes)),
+                              static_cast<uint8_t *>(const_cast<void *>(scales)), false, s);
     if (!st && (e = cudaStreamSynchronize(s)) != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack_codes");
     if (st) {
         mq_fp4_free(w);
@@ -279,17 +281,19 @@ mq_status mq_fp4_pack(const void *W, mq_dtype dtype, int64_t E, int64_t N, int64
     if (mq_status st = new_weight(&w)) return st;
     mq_status st = allocate(w, E, N, K, fmt);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    void *rows = nullptr;  // the scales row by row, on the way to their order
+    // codes and scales row by row, on the way to their order
+    uint8_t *rows = nullptr;
+    const int64_t code_bytes = E * N * fp4_code_pitch(K);
     cudaError_t e = cudaSuccess;
     if (!st) {
-        e = cudaMalloc(&rows, static_cast<size_t>(E * N * fp4_scale_pitch(fmt, K)));
+        e = cudaMalloc(reinterpret_cast<void **>(&rows),
+                       static_cast<size_t>(code_bytes + E * N * fp4_scale_pitch(fmt, K)));
         if (e == cudaSuccess) e = cudaMemsetAsync(w->d.err, 0, 4, s);
         if (e != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack");
     }
     if (!st)
-        st = launch_fp4_quantize(W, dtype, E * N, K, K, nullptr, E * N, fmt, w->d.codes, static_cast<uint8_t *>(rows),
-                                 w->d.row_scale, s);
-    if (!st) st = launch_fp4_scale_order(w->d, static_cast<uint8_t *>(rows), false, s);
+        st = launch_fp4_quantize(W, dtype, E * N, K, K, nullptr, E * N, fmt, rows, rows + code_bytes, w->d.row_scale, s);
+    if (!st) st = launch_fp4_order(w->d, rows, rows + code_bytes, false, s);
     if (rows) {
         e = cudaStreamSynchronize(s);
         if (!st && e != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack");
@@ -320,17 +324,16 @@ mq_status mq_fp4_export(const mq_fp4_weight *w, void *codes, void *scales, float
     if (mq_status st = check_quantized(codes, scales, row_scale, d.fmt)) return st;
     if (mq_status st = check_device(w)) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemcpyAsync(codes, d.codes, d.E * d.N * d.pitch, cudaMemcpyDeviceToDevice, s);
-    if (e == cudaSuccess)
-        e = cudaMemsetAsync(scales, 0, d.E * d.N * fp4_scale_pitch(d.fmt, d.K), s);
+    // the scales' padding past the last stage has no place in the pieces
+    cudaError_t e = cudaMemsetAsync(scales, 0, d.E * d.N * fp4_scale_pitch(d.fmt, d.K), s);
     if (e == cudaSuccess && d.row_scale)
         e = cudaMemcpyAsync(row_scale, d.row_scale, d.E * d.N * 4, cudaMemcpyDeviceToDevice, s);
     if (e != cudaSuccess) return cuda_fail(e, "mq_fp4_export");
-    return launch_fp4_scale_order(d, static_cast<uint8_t *>(scales), true, s);
+    return launch_fp4_order(d, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), true, s);
 }
 
 int64_t mq_fp4_workspace_bytes(const mq_fp4_weight *w, int64_t rows) {
-    if (!w || rows <= 0 || rows > kMaxRows) return 0;
+    if (!w || rows <= 0 || rows > kMaxRows || fp4_linear_quantises(w->d, rows)) return 0;
     return Workspace(rows, w->d.K, w->d.fmt).total;
 }
 

@@ -18,6 +18,33 @@ __device__ __forceinline__ void drain_after_abort(const int *abort_flag) {
     }
 }
 
+// An integer that an earlier launch may have written: the volatile load stays
+// behind the wait for that launch.
+__device__ __forceinline__ int load_i32(const int32_t *p) {
+    int v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_f32(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint4 load_u128(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 load_u64(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+    return v;
+}
+
 // Tiles in order: matrix by matrix, each with ceil(rows / TT) token tiles for
 // each of its NT row tiles; the token tiles of one row tile are neighbours,
 // so that its codes come from L2 again. Each warp walks for itself (all lanes
@@ -49,8 +76,8 @@ struct TileWalk {
             int a = 0, b = 0;
             if (e < E) {
                 // entries out of range or order are clamped, never followed
-                a = min(max(__ldg(offsets + e), 0), R);
-                b = min(max(__ldg(offsets + e + 1), a), R);
+                a = min(max(load_i32(offsets + e), 0), R);
+                b = min(max(load_i32(offsets + e + 1), a), R);
             }
             const long long mine = static_cast<long long>((b - a + TT - 1) / TT) * NT;
             long long sum = mine;
@@ -93,6 +120,45 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Sixteen tokens' outputs of this lane's weight row n (v; `left` of them are
+// real, `live`: n < N) into Y [tokens][ldy], whose first token is m. With
+// `paired` (N, ldy and Y's address even) neighbouring lanes trade halves
+// first: even lanes store two rows of the even tokens, odd lanes two rows of
+// the odd ones, 4 bytes a lane and two tokens a warp's store. Called by whole
+// warps.
+__device__ __forceinline__ void store_chunk(const float (&v)[16], void *Y, long long ldy, long long m, long long n,
+                                            int left, bool live, bool paired, bool fp16) {
+    if (paired) {
+        const int odd = threadIdx.x & 1;
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const uint32_t mine = fp16 ? pack_f16(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+            w[j / 2] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+        }
+        // ldy words of 4 bytes: two rows of 16-bit values
+        uint32_t *y = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(Y) + (m + odd) * ldy + (n - odd));
+        if (left >= 16) {
+            if (live) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j, y += ldy) *y = w[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j, y += ldy)
+                if (live && 2 * j + odd < left) *y = w[j];
+        }
+        return;
+    }
+    uint16_t *y = static_cast<uint16_t *>(Y) + m * ldy + n;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, y += ldy) {
+        const uint32_t b = fp16 ? pack_f16(v[j], 0.0f) : pack_bf16(v[j], 0.0f);
+        if (live && j < left) *y = static_cast<uint16_t>(b);
+    }
+}
+
 // Bulk copy of `bytes` (a multiple of 16) into shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -114,15 +180,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Tiled loads into this CTA's shared memory that complete on a barrier of
+// Tiled load into this CTA's shared memory that completes on a barrier of
 // either CTA of a pair (given by in_cta).
-__device__ __forceinline__ void tma_pair_load_3d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
 __device__ __forceinline__ void tma_pair_load_2d(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "

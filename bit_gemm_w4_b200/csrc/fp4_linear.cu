@@ -1,137 +1,173 @@
 // Products with a microscaled 4-bit weight, narrow form: few tokens, where
-// the weight's bytes from HBM are the bound.
+// the weight's bytes from HBM and the latency of a launch are the bound.
 //
 //   Y[r][n] = fx[r] * fw[n] * sum_k (cx[r][k] sx[r][k / B]) (cw[n][k] sw[n][k / B])
 //
 // The weight is the MMA's A operand (128 rows a tile), the tokens its B
-// operand (16, 32, 64 or 128 columns), so that a single token fills a tile of
-// the tensor core; block scales are applied inside the MMA and the 32-bit row
+// operand (16 to 64 columns), so that a single token fills a tile of the
+// tensor core; block scales are applied inside the MMA and the 32-bit row
 // factors (MQ_FP4_NV) when Y is stored. One CTA computes one tile over a share
-// of K; the CTAs of a cluster share a tile and add their partial sums through
-// distributed shared memory in rank order, so that results do not depend on
-// timing.
+// of K; the CTAs of a cluster share a tile, push their partial sums into the
+// shared memory of the CTA that owns the rows, and each owner adds them in
+// rank order, so that results do not depend on timing.
 //
 // Warp 0 copies codes and weight scales (TMA), warp 1 issues scale copies to
-// tensor memory and MMAs, warps 2 and 3 place the tokens' scales (row-major in
-// memory) in the order the tensor core takes, and warps 2 to 5 are the
-// epilogue.
+// tensor memory and MMAs, warps 2 to 9 bring what the tokens need and are the
+// epilogue. The tokens come in two forms: quantised before (their codes by
+// TMA, their row-major scales placed in the tensor core's order by warps 2 to
+// 9), or as they are, quantised by warps 2 to 9 on the way into shared memory,
+// which saves a launch and the round through memory where few tokens would be
+// quantised by every CTA alike.
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "fp4.h"
+#include "fp4_convert.cuh"
 #include "fp4_device.cuh"
 #include "tc5.cuh"
 
 namespace mq {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
+constexpr int kFeeders = 256;  // threads of warps 2 to 9
 constexpr int kMaxStages = 8;
-constexpr int kBoxRows = 16;  // tokens of one copy
-constexpr int kATile = 128 * 128;
+constexpr int kBoxRows = 16;   // tokens of one copy
+constexpr int kMaxTT = 64;
 
 struct NarrowParams {
-    CUtensorMap tw, tx;
-    const uint8_t *wscales;
+    CUtensorMap tx;
+    const uint8_t *pieces;
     const float *wfactor;
-    const uint8_t *xscales;
+    const uint8_t *xscales;  // quantised tokens
     const float *xfactor;
+    long long xspitch;
+    const void *X;           // tokens as they are
+    long long ldx, x_rows;
+    const int32_t *index;
+    RowSource from;
     const int32_t *offsets;
     void *Y;
-    long long ldy, xspitch;
+    long long ldy;
     int *err;
     long long N;
     int NT, KS, E, R;
-    int TT;      // tokens of a tile: 16, 32, 64 or 128
+    int TT;      // tokens of a tile: 16, 32 or 64
     int split;   // CTAs that share a tile (the cluster)
     int stages;  // ring slots
-    int fp16;
-    int chained;
+    int fp16;    // Y's type
+    int paired;  // N, the stride and Y's address are even: 4-byte stores
 };
 
-// Shared memory: the ring (codes of A and B, scales of A and B in each slot),
-// then barriers.
+// Shared memory: the ring (a piece of the weight, the tokens' codes and scales
+// in each slot),
+// partial sums from the cluster, the tokens' factors, barriers.
 template <bool NV>
 struct NarrowSmem {
-    static constexpr int kUnits = NV ? 4 : 2;      // 512-byte scale units of 128 rows in a stage
+    static constexpr int kUnits = NV ? 4 : 2;  // 512-byte scale units of 128 rows in a stage
     static constexpr int kScales = kUnits * 512;
-    __host__ __device__ static int slot(int TT) { return kATile + TT * 128 + 2 * kScales; }
-    __host__ __device__ static int total(int TT, int stages) { return slot(TT) * stages + 1024 + 256; }
+    static constexpr int kPiece = kFp4CodePiece + kScales;
+    __host__ __device__ static int slot(int TT) { return kPiece + TT * 128 + kScales; }
+    __host__ __device__ static int width(int split) { return (128 + split - 1) / split; }
+    __host__ __device__ static int recv(int TT, int split) {
+        return split > 1 ? (split * width(split) * TT * 4 + 127) / 128 * 128 : 0;
+    }
+    // Partial sums of up to 32 tokens have room of their own; more go where
+    // the ring was, once every CTA of the cluster is done with it.
+    __host__ __device__ static bool apart(int TT) { return TT <= 32; }
+    __host__ __device__ static int fixed(int TT, int split) { return (apart(TT) ? recv(TT, split) : 0) + kMaxTT * 12 + 512 + 256 + 1024; }
+    __host__ __device__ static int total(int TT, int split, int stages) { return slot(TT) * stages + fixed(TT, split); }
 };
 
-template <bool NV>
+// T: void for tokens quantised before, else their type.
+template <bool NV, class T>
 __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_constant__ NarrowParams p) {
     using S = NarrowSmem<NV>;
+    constexpr bool kQuantise = !std::is_same<T, void>::value;
     constexpr int kUnits = S::kUnits;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int TT = p.TT, stages = p.stages, slot = S::slot(TT);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + slot * stages);
-    uint64_t *full = bars, *empty = bars + kMaxStages, *done = bars + 2 * kMaxStages;
+    const int split = p.split, rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int at_b = S::kPiece, at_sb = at_b + TT * 128;
+    float *recv = reinterpret_cast<float *>(smem + (S::apart(TT) ? slot * stages : 0));
+    float *factors =
+        reinterpret_cast<float *>(smem + slot * stages + (S::apart(TT) ? S::recv(TT, split) : 0));  // [TT]
+    uint32_t *tops = reinterpret_cast<uint32_t *>(factors + kMaxTT);                        // [TT]
+    int *sources = reinterpret_cast<int *>(tops + kMaxTT);                                  // [TT]
+    float *wfactors = reinterpret_cast<float *>(sources + kMaxTT);                          // [128]
+    uint64_t *full = reinterpret_cast<uint64_t *>(wfactors + 128);
+    uint64_t *empty = full + kMaxStages, *done = empty + kMaxStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
-    int *info = abort_flag + 1;  // expert, token begin, tokens, row tile, live
 
-    const int split = p.split, rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
-    if (warp == 0) {
-        Tile t{0, 0, 0, 0};
-        TileWalk walk(p.offsets, p.E, p.R, TT, p.NT);
-        const bool live = walk.find(blockIdx.x / split, t);
-        if (lane == 0) {
-            info[0] = t.e;
-            info[1] = t.m0;
-            info[2] = t.tokens;
-            info[3] = t.nt;
-            info[4] = live ? 1 : 0;
-            for (int s = 0; s < stages; ++s) {
-                mbar_init(&full[s], 3);
-                mbar_init(&empty[s], 1);
-            }
-            mbar_init(done, 1);
-            *abort_flag = 0;
-            fence_mbar_init();
+    if (split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1 + kFeeders / 32);
+            mbar_init(&empty[s], 1);
         }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        if constexpr (!kQuantise) prefetch_tensormap(&p.tx);
     }
-    const uint32_t tmem_cols = TT <= 64 ? 128 : 256;
+    if constexpr (kQuantise)
+        if (threadIdx.x >= 64)
+            for (int i = threadIdx.x - 64; i < TT; i += kFeeders) tops[i] = 0;
+    // Offsets may come from the launch just before; a chained launch starts
+    // only when the one that quantised its tokens has seen them complete.
+    if (kQuantise && p.offsets) pdl_wait();
+    Tile t{0, 0, 0, 0};
+    TileWalk walk(p.offsets, p.E, p.R, TT, p.NT);
+    const bool live = walk.find(blockIdx.x / split, t);  // the same in every CTA of a cluster
+    const int m0 = t.m0, tokens = t.tokens, n0 = t.nt * 128;
+    const int nb = (tokens + kBoxRows - 1) / kBoxRows;
+    const int k0 = static_cast<int>(static_cast<long long>(p.KS) * rank / split);
+    const int nk = static_cast<int>(static_cast<long long>(p.KS) * (rank + 1) / split) - k0;
+    const int ahead = min(stages, nk);  // stages that fill the ring without waiting
+    auto weight = [&](int i, int s) {
+        mbar_arrive_expect_tx(&full[s], S::kPiece + (kQuantise ? 0 : nb * kBoxRows * 128));
+        bulk_load(smem + s * slot,
+                  p.pieces + ((static_cast<long long>(t.e) * p.NT + t.nt) * p.KS + k0 + i) * S::kPiece, S::kPiece,
+                  &full[s]);
+    };
+    // the weight does not depend on the launch before: its first stages go ahead
+    if (warp == 0) {
+        __syncwarp();
+        if (live && tc5::elect())
+            for (int i = 0; i < ahead; ++i) weight(i, i);
+        __syncwarp();
+    }
+    if constexpr (NV)
+        if (threadIdx.x >= 64 && threadIdx.x < 64 + 128 && live) {
+            const int row = threadIdx.x - 64;
+            wfactors[row] = n0 + row < p.N ? __ldg(p.wfactor + static_cast<long long>(t.e) * p.N + n0 + row) : 0.0f;
+        }
+    constexpr uint32_t tmem_cols = 128;
     if (warp == 1) tc5::alloc<1>(tmem_slot, tmem_cols);
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int expert = info[0], m0 = info[1], tokens = info[2], n0 = info[3] * 128;
-    const bool live = info[4] != 0;  // the same in every CTA of a cluster
-    const int nb = (tokens + kBoxRows - 1) / kBoxRows;
-    const int k0 = static_cast<int>(static_cast<long long>(p.KS) * rank / split);
-    const int nk = static_cast<int>(static_cast<long long>(p.KS) * (rank + 1) / split) - k0;
 
     if (!live) {
         // nothing to do
     } else if (warp == 0) {
-        const uint32_t bytes = kATile + S::kScales + nb * kBoxRows * 128;
-        const uint8_t *ws = p.wscales + ((static_cast<long long>(expert) * p.NT + info[3]) * p.KS + k0) * S::kScales;
-        auto weight = [&](int i, int s) {
-            uint8_t *at = smem + s * slot;
-            mbar_arrive_expect_tx(&full[s], bytes);
-            tma_load_3d(at, &p.tw, &full[s], (k0 + i) * 128, n0, expert);
-            bulk_load(at + kATile + TT * 128, ws + static_cast<long long>(i) * S::kScales, S::kScales, &full[s]);
-        };
         auto tokens_in = [&](int i, int s) {
             for (int b = 0; b < nb; ++b)
-                tma_load_2d(smem + s * slot + kATile + b * kBoxRows * 128, &p.tx, &full[s], (k0 + i) * 128,
+                tma_load_2d(smem + s * slot + at_b + b * kBoxRows * 128, &p.tx, &full[s], (k0 + i) * 128,
                             m0 + b * kBoxRows);
         };
-        // the weight does not depend on the launch before: its first stages go ahead
-        const int ahead = min(stages, nk);
-        if (tc5::elect())
-            for (int i = 0; i < ahead; ++i) weight(i, i);
-        __syncwarp();
-        pdl_wait();
-        if (tc5::elect())
-            for (int i = 0; i < ahead; ++i) tokens_in(i, i);
-        __syncwarp();
+        if constexpr (!kQuantise) {
+            pdl_wait();
+            if (tc5::elect())
+                for (int i = 0; i < ahead; ++i) tokens_in(i, i);
+            __syncwarp();
+        }
         bool ok = true;
         for (int i = ahead, s = 0, ph = 0; i < nk && ok; ++i) {
             ok = mbar_wait(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag);
@@ -139,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
             if (!ok) break;
             if (tc5::elect()) {
                 weight(i, s);
-                tokens_in(i, s);
+                if constexpr (!kQuantise) tokens_in(i, s);
             }
             __syncwarp();
             if (++s == stages) s = 0, ph ^= 1;
@@ -154,8 +190,8 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
             if (!ok) break;
             tc5::fence_after();
             const uint32_t at = smem_u32(smem) + s * slot;
-            const uint32_t sa = at + kATile + TT * 128, sb = sa + S::kScales;
-            const uint64_t da = tc5::operand_desc(at), db = tc5::operand_desc(at + kATile);
+            const uint32_t sa = at + kFp4CodePiece, sb = at + at_sb;
+            const uint64_t da = tc5::operand_desc(at), db = tc5::operand_desc(at + at_b);
             if (tc5::elect()) {
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) {
@@ -176,103 +212,219 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
         }
         if (tc5::elect()) tc5::commit(done);
         __syncwarp();
-    } else if (warp < 4) {
-        // the tokens' scales: 4-byte pieces into the tensor core's order. A
-        // stage is handed over two iterations after its copies were issued.
-        pdl_wait();
-        auto place = [&](int i, int s) {
-            uint8_t *at = smem + s * slot + kATile + TT * 128 + S::kScales;
-            for (int r = threadIdx.x - 64; r < tokens; r += 64) {
-                const uint8_t *src = p.xscales + (m0 + r) * p.xspitch + static_cast<long long>(k0 + i) * (4 * kUnits);
-                uint8_t *dst = at + (r & 31) * 16 + (r >> 5) * 4;
-#pragma unroll
-                for (int u = 0; u < kUnits; ++u) cp_async4(dst + 512 * u, src + 4 * u);
-            }
-            cp_async_commit();
-        };
+    } else {
+        const int tid = threadIdx.x - 64;
+        // a stage's tokens are written: order that before the tensor core's reads
         auto hand_over = [&](int s) {
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[s]);
         };
-        int s = 0, ph = 1, hs = 0;
-        for (int i = 0; i < nk; ++i) {
-            if (!mbar_wait_warp(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag)) break;
-            place(i, s);
-            if (++s == stages) s = 0, ph ^= 1;
-            if (i >= 2) {
-                cp_async_wait_group<2>();
-                hand_over(hs);
-                if (++hs == stages) hs = 0;
-            }
-        }
-        if (nk >= 2) {
-            cp_async_wait_group<1>();
-            hand_over(hs);
-            if (++hs == stages) hs = 0;
-        }
-        cp_async_wait_group<0>();
-        hand_over(hs);
-    }
-
-    __syncwarp();
-
-    // ------------------------------------------------------------ epilogue
-    if (live && warp >= 2) {
-        const int quad = warp & 3, row = quad * 32 + lane;
         pdl_wait();
-        __syncwarp();
-        mbar_wait_warp(done, 0, p.err, kErrWaitMma, abort_flag);
-        tc5::fence_after();
-        const long long n = n0 + row;
-        const float fw = NV && n < p.N ? __ldg(p.wfactor + static_cast<long long>(expert) * p.N + n) : 1.0f;
-        float *part = reinterpret_cast<float *>(smem);  // [tokens][128], the ring is drained
-        for (int c = 0; c < nb * kBoxRows; c += 16) {
-            uint32_t bits[16];
-            tc5::load16(tmem + (static_cast<uint32_t>(quad) << 21) + c, bits);
-            tc5::load_wait();
-            float v[16];
+        if constexpr (kQuantise) {
+            if (tid < tokens) sources[tid] = p.index ? load_i32(p.index + m0 + tid) : m0 + tid;
+            asm volatile("bar.sync 1, %0;" ::"n"(kFeeders) : "memory");
+            auto chunk = [&](int r, long long c) {
+                Raw<T> raw;
+                const long long x = sources[r];
+                if (x >= 0 && x < p.x_rows)
+                    load_chunk(raw, p.from, static_cast<const T *>(p.X) + x * p.ldx, c);
+                else
+                    raw.clear();
+                return raw;
+            };
+            if constexpr (NV) {
+                // the rows' largest magnitudes over all of K, a warp a row, or
+                // the warps shared out over a few rows
+                const int chunks = static_cast<int>((p.from.K + kChunk - 1) / kChunk);
+                const int parts = tokens == 1 ? 8 : tokens == 2 ? 4 : tokens <= 4 ? 2 : 1;
+                for (int x = warp - 2; x < tokens * parts; x += kFeeders / 32) {
+                    const int r = x / parts;
+                    uint32_t m = 0;
+#pragma unroll 4
+                    for (int c = (x - r * parts) * 32 + lane; c < chunks; c += 32 * parts)
+                        m = max(m, chunk(r, static_cast<long long>(c) * kChunk).max_bits());
+                    m = __reduce_max_sync(0xffffffffu, m);
+                    if (lane == 0) atomicMax(&tops[r], m);
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(kFeeders) : "memory");
+                if (tid < tokens) {
+                    float inverse;
+                    factors[tid] = nv_factor<T>(tops[tid], inverse);
+                }
+            }
+            const int per = tokens * 16;  // chunks of a stage
+            auto read = [&](int i, int w) {
+                Raw<T> raw;
+                raw.clear();
+                if (w < per) raw = chunk(w >> 4, static_cast<long long>(k0 + i) * kFp4StageK + (w & 15) * kChunk);
+                return raw;
+            };
+            // chunk w of a stage into slot s; called by whole warps, w >= per does nothing
+            auto place = [&](const Raw<T> &raw, int s, int w) {
+                const int r = w < per ? w >> 4 : 0, c = w & 15;
+                uint8_t *at = smem + s * slot;
+                uint32_t top = raw.max_bits(), scale;
+                int unit = c >> 2, byte = c & 3;
+                float inv;
+                if constexpr (NV) {
+                    float inverse;
+                    const float factor = nv_factor<T>(tops[r], inverse);
+                    scale = nv_scale<T>(top, factor, inverse, inv);
+                } else {
+                    // lanes 2i and 2i + 1 hold the two halves of a block
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    scale = mx_scale<T>(top, inv);
+                    unit = c >> 3, byte = (c >> 1) & 3;
+                }
+                if (w >= per) return;
+                at[at_sb + unit * 512 + r * 16 + byte] = static_cast<uint8_t>(scale);
+                // 16-byte unit c / 2 of the row, under the 128-byte swizzle
+                *reinterpret_cast<uint2 *>(at + at_b + r * 128 + (((c >> 1) ^ (r & 7)) * 16) + (c & 1) * 8) =
+                    codes_of(raw, inv);
+            };
+            // stages that need no slot to be given back: all their chunks at once
+            for (int x = tid; x - lane < ahead * per; x += kFeeders) {
+                const int i = min(x / per, ahead), w = i < ahead ? x - i * per : per + (x & 1);
+                place(read(i, w), i < ahead ? i : 0, w);
+            }
+            for (int i = 0; i < ahead; ++i) hand_over(i);
+            // the others one by one, a stage's elements read ahead of its turn;
+            // a thread has at most one chunk of up to 16 tokens
+            Raw<T> next;
+            if (ahead < nk) next = read(ahead, tid);
+            for (int i = ahead, s = 0, ph = 0; i < nk; ++i) {
+                const Raw<T> now = next;
+                if (i + 1 < nk) next = read(i + 1, tid);
+                if (!mbar_wait_warp(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag)) break;
+                place(now, s, tid);
+                hand_over(s);
+                if (++s == stages) s = 0, ph ^= 1;
+            }
+        } else {
+            if constexpr (NV)
+                for (int r = tid; r < tokens; r += kFeeders) factors[r] = load_f32(p.xfactor + m0 + r);
+            // scales: a row's of four stages (64 or 32 bytes) are read in one
+            // go, one group of stages ahead of their turn
+            constexpr int kGroup = 4, kVecs = NV ? 4 : 2;
+            uint4 next[kVecs];
+            auto fetch = [&](int i) {
+                if (tid >= tokens) return;
+                const uint8_t *src = p.xscales + (m0 + tid) * p.xspitch + static_cast<long long>(k0 + i) * (4 * kUnits);
+                if constexpr (NV) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(bits[j]);
-            if (split > 1) {
+                    for (int v = 0; v < kVecs; ++v)
+                        if (i + v < nk) next[v] = load_u128(src + 16 * v);
+                } else {
+                    // an 8-byte step: two stages may lie across 16-byte units
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (c + j < tokens) part[(c + j) * 128 + row] = v[j];
-            } else if (n < p.N) {
+                    for (int v = 0; v < kGroup; ++v)
+                        if (i + v < nk) {
+                            const uint2 w = load_u64(src + 8 * v);
+                            if (v & 1)
+                                next[v >> 1].z = w.x, next[v >> 1].w = w.y;
+                            else
+                                next[v >> 1].x = w.x, next[v >> 1].y = w.y;
+                        }
+                }
+            };
+            fetch(0);
+            int s = 0, ph = 1;
+            bool ok = true;
+            for (int i = 0; i < nk && ok; i += kGroup) {
+                uint4 now[kVecs];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int t = c + j;
-                    if (t >= tokens) break;
-                    float y = v[j];
-                    if constexpr (NV) y = y * p.xfactor[m0 + t] * fw;
-                    store_output(p.Y, (m0 + t) * p.ldy + n, y, p.fp16);
+                for (int v = 0; v < kVecs; ++v) now[v] = next[v];
+                if (i + kGroup < nk) fetch(i + kGroup);
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) {
+                    if (i + j >= nk) break;
+                    ok = mbar_wait_warp(&empty[s], ph, p.err, kErrWaitEmpty, abort_flag);
+                    if (!ok) break;
+                    if (tid < tokens) {
+                        uint32_t *dst =
+                            reinterpret_cast<uint32_t *>(smem + s * slot + at_sb + (tid & 31) * 16 + (tid >> 5) * 4);
+                        if constexpr (NV) {
+                            dst[0] = now[j].x;
+                            dst[128] = now[j].y;
+                            dst[256] = now[j].z;
+                            dst[384] = now[j].w;
+                        } else {
+                            dst[0] = j & 1 ? now[j >> 1].z : now[j >> 1].x;
+                            dst[128] = j & 1 ? now[j >> 1].w : now[j >> 1].y;
+                        }
+                    }
+                    hand_over(s);
+                    if (++s == stages) s = 0, ph ^= 1;
                 }
             }
         }
     }
-    drain_after_abort(abort_flag);
     __syncwarp();
-    if (live && split > 1) {
-        cluster_sync();
-        if (warp >= 2) {
-            // rank r adds the elements [r, r + 1) / split of the tile
-            const float *part = reinterpret_cast<const float *>(smem);
-            const int total = tokens * 128;
-            const int lo = static_cast<int>(static_cast<long long>(total) * rank / split);
-            const int hi = static_cast<int>(static_cast<long long>(total) * (rank + 1) / split);
-            for (int i = lo + threadIdx.x - 64; i < hi; i += 128) {
-                const int t = i >> 7;
-                const long long n = n0 + (i & 127);
-                float y = 0.0f;
-                for (int r = 0; r < split; ++r) y += ld_dsmem_f32(part + i, r);
-                if (n >= p.N) continue;
-                if constexpr (NV)
-                    y = y * p.xfactor[m0 + t] * __ldg(p.wfactor + static_cast<long long>(expert) * p.N + n);
-                store_output(p.Y, (m0 + t) * p.ldy + n, y, p.fp16);
-            }
-        }
+
+    // ------------------------------------------------------------ epilogue
+    if (split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has started
+    const int first = 128 * rank / split, width = 128 * (rank + 1) / split - first;  // the rows this CTA adds up
+    const int W = S::width(split);
+    if (live && warp >= 2) {
+        asm volatile("bar.sync 1, %0;" ::"n"(kFeeders) : "memory");  // the factors are written
+        mbar_wait_warp(done, 0, p.err, kErrWaitMma, abort_flag);
+        tc5::fence_after();
+    }
+    if (split > 1 && !S::apart(TT)) {
+        __syncwarp();
         cluster_sync();
     }
+    if (live && warp >= 2) {
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const long long n = n0 + row;
+        const int owner = ((row + 1) * split - 1) / 128;
+        uint32_t to = 0;
+        if (split > 1) to = in_cta(recv + rank * TT * W + row - 128 * owner / split, owner);
+        // two warps share a quarter of the lanes: every other chunk of tokens each
+        for (int c = 16 * ((warp - 2) >> 2); c < tokens; c += 32) {
+            uint32_t bits[16];
+            tc5::load16(tmem + (static_cast<uint32_t>(quad) << 21) + c, bits);
+            tc5::load_wait();
+            const int left = tokens - c;
+            if (split > 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < left)
+                        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + (c + j) * W * 4), "r"(bits[j])
+                                     : "memory");
+                continue;
+            }
+            float v[16];
+            const float fw = NV ? wfactors[row] : 1.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                v[j] = __uint_as_float(bits[j]);
+                if constexpr (NV) v[j] = v[j] * factors[c + j] * fw;
+            }
+            store_chunk(v, p.Y, p.ldy, m0 + c, n, left, n < p.N, p.paired, p.fp16);
+        }
+    }
+    drain_after_abort(abort_flag);
+    __syncwarp();
+    if (split > 1) {
+        cluster_sync();  // every partial sum has arrived; nobody reaches into another CTA after this
+        if (live && warp >= 2) {
+            for (int i = threadIdx.x - 64; i < tokens * width; i += kFeeders) {
+                const int m = i / width, w = i - m * width;
+                const long long n = n0 + first + w;
+                float part[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) part[r] = r < split ? recv[(r * TT + m) * W + w] : 0.0f;
+                float y = part[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r) y += part[r];  // those past `split` are zeros
+                if constexpr (NV) y = y * factors[m] * wfactors[first + w];
+                if (n < p.N) store_output(p.Y, (m0 + m) * p.ldy + n, y, p.fp16);
+            }
+        }
+    }
+    pdl_wait();  // a launch is not over before the one it was chained to
     tc5::fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -281,45 +433,39 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
     }
 }
 
-template <bool NV>
-mq_status run_narrow(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,
-                     int64_t ldy, bool chained, cudaStream_t stream) {
+template <bool NV, class T>
+mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, int64_t likely, bool chained,
+                     cudaStream_t stream) {
     using S = NarrowSmem<NV>;
-    NarrowParams p{};
-    const int64_t per = offsets ? (x.rows + d.E - 1) / d.E : x.rows;  // rows of an average matrix
-    p.TT = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+    p.TT = TT;
     // the most tiles that any split of the rows into matrices makes
-    const int64_t tiles = (offsets ? std::min<int64_t>(d.E, x.rows) + x.rows / p.TT : (x.rows + p.TT - 1) / p.TT) * d.NT;
-    const int64_t likely = (offsets ? std::min<int64_t>(d.E, x.rows) * ((per + p.TT - 1) / p.TT)
-                                    : (x.rows + p.TT - 1) / p.TT) * d.NT;
-    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, 2 * sm_count() / std::max<int64_t>(1, likely)})));
+    const int64_t tiles = (p.offsets ? std::min<int64_t>(d.E, rows) + rows / p.TT : (rows + p.TT - 1) / p.TT) * d.NT;
+    // Two CTAs an SM where each then has a ring of four stages, else one. K is
+    // split as far as that gives every SM at most one CTA: past it the further
+    // CTAs start after the first ones' loads (1 x 4096 x 4096 takes 9.1, 8.0,
+    // 8.5 and 9.3 us with 2, 4, 6 and 8; 1 x 11008 x 4096, 86 tiles, 11.8 us
+    // with 1 and 14.0 us with 4).
+    const int each = (113 * 1024 - S::fixed(p.TT, 8)) / S::slot(p.TT) >= 4 ? 2 : 1;
+    const int budget = each == 2 ? 113 * 1024 : 227 * 1024;
+    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sm_count() / likely})));
     if (tiles * p.split > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 linear: too many tiles");
-    p.stages = std::min(kMaxStages, std::max(3, (112 * 1024 - 1280) / S::slot(p.TT)));
-    const int smem = S::total(p.TT, p.stages);
-    p.tw = d.map;
-    if (!encode_bytes_map(&p.tx, x.codes, d.pitch, x.rows, 0, kBoxRows))
-        return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activations");
-    p.wscales = d.scales;
+    p.stages = std::min(kMaxStages, (budget - S::fixed(p.TT, p.split)) / S::slot(p.TT));
+    const int smem = S::total(p.TT, p.split, p.stages);
+    p.pieces = d.pieces;
     p.wfactor = d.row_scale;
-    p.xscales = x.scales;
-    p.xfactor = x.row_scale;
-    p.offsets = offsets;
-    p.Y = Y;
-    p.ldy = ldy;
-    p.xspitch = fp4_scale_pitch(d.fmt, d.K);
     p.err = d.err;
     p.N = d.N;
     p.NT = static_cast<int>(d.NT);
     p.KS = d.KS;
     p.E = static_cast<int>(d.E);
-    p.R = static_cast<int>(x.rows);
-    p.fp16 = dtype == MQ_FP16;
+    p.R = static_cast<int>(rows);
+    p.paired = d.N % 2 == 0 && p.ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 3) == 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(MQ_ERR_CUDA, "cudaGetDevice failed");
     if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
     static bool configured[64] = {};
     if (!configured[dev]) {
-        if (cudaFuncSetAttribute(fp4_narrow_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+        if (cudaFuncSetAttribute(fp4_narrow_kernel<NV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
             cudaSuccess)
             return fail(MQ_ERR_CUDA, "fp4 linear: device setup failed");
         configured[dev] = true;
@@ -345,9 +491,30 @@ mq_status run_narrow(const Fp4Device &d, const Fp4Rows &x, const int32_t *offset
     }
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_narrow_kernel<NV>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_narrow_kernel<NV, T>, p);
     if (e != cudaSuccess) return fail(MQ_ERR_CUDA, std::string("fp4 linear launch: ") + cudaGetErrorString(e));
     return MQ_OK;
+}
+
+// How a product is run, from its sizes alone (the rows of each matrix are not
+// known to the host: `per` is their average).
+struct Choice {
+    int TT;          // tokens of a narrow tile; 0: the wide form
+    int64_t likely;  // narrow tiles of the matrices that have rows
+};
+
+Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
+    const int64_t mats = grouped ? std::min<int64_t>(d.E, rows) : 1, per = (rows + mats - 1) / mats;
+    const int64_t sms = sm_count();
+    // Up to 32 tokens: narrow, as long as its tiles run in one wave of two CTAs
+    // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
+    // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 64: narrow
+    // where K can be split between CTAs, which the wide form does not do (64 x
+    // 4096 x 11008: 14.4 us, wide 20.1; 64 x 11008 x 4096: 12.1 us, wide 11.6).
+    const int TT = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+    const int64_t likely = mats * d.NT;
+    if (per <= 32 ? likely <= 2 * sms : per <= 64 && likely <= sms / 2) return {TT, likely};
+    return {0, likely};
 }
 
 }  // namespace
@@ -355,10 +522,53 @@ mq_status run_narrow(const Fp4Device &d, const Fp4Rows &x, const int32_t *offset
 mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                             mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream) {
     if (x.rows <= 0) return MQ_OK;
-    const int64_t per = offsets ? x.rows / std::min<int64_t>(d.E, x.rows) : x.rows;  // rows of a matrix
-    if (per > 128) return launch_fp4_wide(d, x, offsets, Y, dtype, ldy, chained, stream);
-    return d.fmt == MQ_FP4_NV ? run_narrow<true>(d, x, offsets, Y, dtype, ldy, chained, stream)
-                              : run_narrow<false>(d, x, offsets, Y, dtype, ldy, chained, stream);
+    const Choice c = choose(d, x.rows, d.E > 1);
+    if (!c.TT) return launch_fp4_wide(d, x, offsets, Y, dtype, ldy, chained, stream);
+    NarrowParams p{};
+    if (!encode_bytes_map(&p.tx, x.codes, fp4_code_pitch(d.K), x.rows, kBoxRows, true))
+        return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activations");
+    p.xscales = x.scales;
+    p.xfactor = x.row_scale;
+    p.xspitch = fp4_scale_pitch(d.fmt, d.K);
+    p.offsets = offsets;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.fp16 = dtype == MQ_FP16;
+    return d.fmt == MQ_FP4_NV ? run_narrow<true, void>(d, p, x.rows, c.TT, c.likely, chained, stream)
+                              : run_narrow<false, void>(d, p, x.rows, c.TT, c.likely, chained, stream);
+}
+
+// One or two rows a matrix and little weight to read: the launch saved is
+// worth what every CTA's own quantisation costs (1 x 4096 x 4096: 8.4 us of the
+// device's time against 8.0 us, and one launch of the host's instead of two;
+// at four rows it is 9.4 against 7.9 us).
+bool fp4_linear_quantises(const Fp4Device &d, int64_t rows) {
+    const Choice c = choose(d, rows, d.E > 1);
+    const int64_t mats = std::min<int64_t>(d.E, rows);
+    return c.TT == 16 && rows <= 2 * mats && c.likely * d.KS * fp4_piece(d.fmt) <= (int64_t(40) << 20) &&
+           (d.fmt == MQ_FP4_MX || d.K <= 16384);
+}
+
+mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype dtype, int64_t rows, int64_t ldx,
+                                   const int32_t *index, int64_t x_rows, const int32_t *offsets, void *Y,
+                                   int64_t ldy, cudaStream_t stream) {
+    if (rows <= 0) return MQ_OK;
+    const Choice c = choose(d, rows, d.E > 1);
+    NarrowParams p{};
+    p.X = X;
+    p.ldx = ldx;
+    p.x_rows = x_rows;
+    p.index = index;
+    p.from = {d.K, static_cast<const char *>(X), static_cast<const char *>(X) + ((x_rows - 1) * ldx + d.K) * 2};
+    p.offsets = offsets;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.fp16 = dtype == MQ_FP16;
+    if (dtype == MQ_FP16)
+        return d.fmt == MQ_FP4_NV ? run_narrow<true, __half>(d, p, rows, 16, c.likely, true, stream)
+                                  : run_narrow<false, __half>(d, p, rows, 16, c.likely, true, stream);
+    return d.fmt == MQ_FP4_NV ? run_narrow<true, __nv_bfloat16>(d, p, rows, 16, c.likely, true, stream)
+                              : run_narrow<false, __nv_bfloat16>(d, p, rows, 16, c.likely, true, stream);
 }
 
 }  // namespace mq

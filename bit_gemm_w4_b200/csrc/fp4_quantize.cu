@@ -9,19 +9,15 @@
 // Both directions are bound by memory: quantising 16-bit X reads 2 bytes and
 // writes 0.53 to 0.56 bytes an element.
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
-#include <type_traits>
 
 #include "common.cuh"
 #include "fp4.h"
+#include "fp4_convert.cuh"
+#include "fp4_device.cuh"
 
 namespace mq {
 namespace {
-
-constexpr int kChunk = 16;  // columns a thread holds at a time
 
 struct QuantArgs {
     const void *X;
@@ -29,172 +25,10 @@ struct QuantArgs {
     const int32_t *index;
     uint8_t *codes, *scales;
     float *row_scale;
-    long long rows, K;
+    long long rows;
     long long cpitch, spitch;  // bytes of a row of codes, of scales
-    const char *x_begin, *x_end;  // the bytes X occupies
+    RowSource from;
 };
-
-// ---------------------------------------------------------------- conversions
-// Eight values to eight E2M1 codes, the first in the low nibble; rounded to
-// nearest even, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1_x8(const float *v) {
-    uint32_t d;
-    asm("{\n\t.reg .b8 a, b, c, e;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 e, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, e};\n\t}"
-        : "=r"(d)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-    return d;
-}
-
-// Eight E2M1 codes to their values as four f16x2 (exact).
-__device__ __forceinline__ void e2m1_values(uint32_t codes, uint32_t (&h)[4]) {
-    asm("{\n\t.reg .b8 a, b, c, e;\n\t"
-        "mov.b32 {a, b, c, e}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, e;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(codes));
-}
-
-__device__ __forceinline__ uint32_t e4m3_bits(float v) {
-    unsigned short d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(0.0f), "f"(v));
-    return d & 0xFFu;
-}
-
-__device__ __forceinline__ float e4m3_value(uint32_t bits) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(bits)));
-    return __low2float(*reinterpret_cast<__half2 *>(&h));
-}
-
-// 2^(s - 127); 255 is NaN.
-__device__ __forceinline__ float e8m0_value(uint32_t s) {
-    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
-}
-
-// ---------------------------------------------------------------- input
-// Sixteen consecutive elements as raw words: 8 for the 16-bit types, 16 for
-// fp32.
-template <class T>
-struct Raw {
-    static constexpr int kWords = kChunk * static_cast<int>(sizeof(T)) / 4;
-    uint32_t w[kWords];
-
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = 0;
-    }
-    // The largest magnitude's bits; an order of non-negative floats is the
-    // order of their bits, infinities and NaN above every finite value.
-    __device__ __forceinline__ uint32_t max_bits() const {
-        if constexpr (sizeof(T) == 2) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-            return max(m & 0xFFFFu, m >> 16);
-        } else {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-            return m;
-        }
-    }
-    __device__ __forceinline__ float value(int i) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        const uint32_t h = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu;
-        return of_bits(h);
-    }
-    // An element's bits (as max_bits gives them) as fp32.
-    static __device__ __forceinline__ float of_bits(uint32_t h) {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(h);
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(h << 16);
-        return half_bits_to_f32(h);
-    }
-};
-
-__device__ __forceinline__ uint4 ldg128(const char *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-// Columns c .. c + 15 of the row at `row`, zeros past K. Rows on 16-byte
-// boundaries are read as they are. Others (a 16-bit type with an odd stride,
-// a view) are read in the aligned 16-byte units that cover the chunk, which
-// lie inside X, and shifted into place; the units that stick out of X at
-// either end, and the last partial chunk, go element by element.
-template <class T>
-__device__ __forceinline__ void load_chunk(Raw<T> &r, const QuantArgs &a, const T *row, long long c) {
-    if (c >= a.K) {
-        r.clear();
-        return;
-    }
-    const char *p = reinterpret_cast<const char *>(row + c);
-    if (c + kChunk <= a.K) {
-        const uint32_t phase = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
-        if (phase == 0) {
-#pragma unroll
-            for (int i = 0; i < Raw<T>::kWords / 4; ++i) {
-                const uint4 v = ldg128(p + 16 * i);
-                r.w[4 * i] = v.x;
-                r.w[4 * i + 1] = v.y;
-                r.w[4 * i + 2] = v.z;
-                r.w[4 * i + 3] = v.w;
-            }
-            return;
-        }
-        if constexpr (sizeof(T) == 2) {
-            const char *q = p - phase;
-            if (q >= a.x_begin && q + 48 <= a.x_end) {
-                uint32_t t[12];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    uint4 v;
-                    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                 : "l"(q + 16 * i));
-                    t[4 * i] = v.x;
-                    t[4 * i + 1] = v.y;
-                    t[4 * i + 2] = v.z;
-                    t[4 * i + 3] = v.w;
-                }
-                // whole words, then half a word
-                if (phase & 8) {
-#pragma unroll
-                    for (int i = 0; i < 10; ++i) t[i] = t[i + 2];
-                }
-                if (phase & 4) {
-#pragma unroll
-                    for (int i = 0; i < 9; ++i) t[i] = t[i + 1];
-                }
-                const uint32_t sh = (phase & 2) * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) r.w[i] = __funnelshift_r(t[i], t[i + 1], sh);
-                return;
-            }
-        }
-    }
-    r.clear();
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        if (c + i >= a.K) break;
-        if constexpr (sizeof(T) == 4) {
-            r.w[i] = __ldg(reinterpret_cast<const unsigned int *>(row) + c + i);
-        } else {
-            const uint32_t h = __ldg(reinterpret_cast<const unsigned short *>(row) + c + i);
-            r.w[i >> 1] |= h << (16 * (i & 1));
-        }
-    }
-}
 
 // ---------------------------------------------------------------- quantise
 // blockDim = (bx, by): bx threads share a row, by rows side by side, kRows
@@ -203,6 +37,8 @@ __device__ __forceinline__ void load_chunk(Raw<T> &r, const QuantArgs &a, const 
 // twice by MQ_FP4_NV, whose row factor needs the whole row first.
 template <class T, bool NV, int kChunks, int kRows>
 __global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
+    // The launch after this one may start once the launches before are over.
+    pdl_wait();
     pdl_launch_dependents();
     constexpr int kMaxWarps = 32;
     __shared__ uint32_t wmax[NV ? kRows * kMaxWarps : 1];
@@ -217,7 +53,7 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
         const long long r = r0 + i;
         src[i] = nullptr;
         if (r < a.rows) {
-            const long long x = a.index ? static_cast<long long>(__ldg(a.index + r)) : r;
+            const long long x = a.index ? static_cast<long long>(load_i32(a.index + r)) : r;
             if (x >= 0 && x < a.x_rows) src[i] = static_cast<const T *>(a.X) + x * a.ldx;
         }
     }
@@ -229,7 +65,7 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
             for (int j = 0; j < kChunks; ++j) {
                 const long long c = (base + tx + static_cast<long long>(j) * bx) * kChunk;
                 if (src[i])
-                    load_chunk(raw[i][j], a, src[i], c);
+                    load_chunk(raw[i][j], a.from, src[i], c);
                 else
                     raw[i][j].clear();
             }
@@ -252,7 +88,7 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
                 for (int j = 0; j < kChunks; ++j) {
                     Raw<T> t;
                     if (src[i])
-                        load_chunk(t, a, src[i], (base + tx + static_cast<long long>(j) * bx) * kChunk);
+                        load_chunk(t, a.from, src[i], (base + tx + static_cast<long long>(j) * bx) * kChunk);
                     else
                         t.clear();
                     m[i] = max(m[i], t.max_bits());
@@ -274,12 +110,7 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const float top = Raw<T>::of_bits(m[i]);
-            const bool finite = top <= 3.402823466e38f;
-            factor[i] = finite ? fmaxf(__fmul_rn(top, static_cast<float>(1.0 / 2688.0)), 0x1p-100f)
-                               : __uint_as_float(0x7FC00000u);
-            // a row that is not finite: NaN as its factor, zeros as its codes and scales
-            inv_factor[i] = finite ? __frcp_rn(factor[i]) : 0.0f;
+            factor[i] = nv_factor<T>(m[i], inv_factor[i]);
             if (tx == 0 && r0 + i < a.rows) a.row_scale[r0 + i] = factor[i];
         }
     }
@@ -296,28 +127,16 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
                 float inv;
                 uint32_t sbits;
                 if constexpr (NV) {
-                    const float t = __fmul_rn(__fmul_rn(Raw<T>::of_bits(top), static_cast<float>(1.0 / 6.0)),
-                                              inv_factor[i]);
-                    sbits = inv_factor[i] > 0.0f ? e4m3_bits(t) : 0u;
-                    inv = sbits ? __frcp_rn(__fmul_rn(e4m3_value(sbits), factor[i])) : 0.0f;
+                    sbits = nv_scale<T>(top, factor[i], inv_factor[i], inv);
                 } else {
                     // lanes 2i and 2i + 1 hold the two halves of a block
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    const uint32_t e = __float_as_uint(Raw<T>::of_bits(top)) >> 23;
-                    const bool finite = e < 255;
-                    const uint32_t s = e > 2 ? e - 2 : 0;
-                    sbits = finite ? s : 255u;
-                    inv = finite ? __uint_as_float((254u - s) << 23) : 0.0f;
+                    sbits = mx_scale<T>(top, inv);
                 }
                 if (r >= a.rows || ch >= chunks) continue;
-                float v[kChunk];
-                const bool zero = inv == 0.0f;  // also keeps infinities times 0 out
-#pragma unroll
-                for (int k = 0; k < kChunk; ++k) v[k] = zero ? 0.0f : __fmul_rn(raw[i][j].value(k), inv);
                 if (ch * 8 < a.cpitch)
-                    *reinterpret_cast<uint2 *>(a.codes + r * a.cpitch + ch * 8) =
-                        make_uint2(e2m1_x8(v), e2m1_x8(v + 8));
-                if (ch * kChunk >= a.K) sbits = 0;
+                    *reinterpret_cast<uint2 *>(a.codes + r * a.cpitch + ch * 8) = codes_of(raw[i][j], inv);
+                if (ch * kChunk >= a.from.K) sbits = 0;
                 if constexpr (NV)
                     a.scales[r * a.spitch + ch] = static_cast<uint8_t>(sbits);
                 else if ((ch & 1) == 0)
@@ -332,8 +151,16 @@ mq_status run_quantize(const QuantArgs &a, int bx, int by, cudaStream_t stream) 
     const long long per = static_cast<long long>(by) * kRows;
     const long long grid = (a.rows + per - 1) / per;
     if (grid > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 quantisation: too many rows");
-    fp4_quantize_kernel<T, NV, kChunks, kRows><<<static_cast<unsigned>(grid), dim3(bx, by), 0, stream>>>(a);
-    const cudaError_t e = cudaPeekAtLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(bx, by);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, NV, kChunks, kRows>, a);
     if (e != cudaSuccess)
         return fail(MQ_ERR_CUDA, std::string("fp4 quantisation launch: ") + cudaGetErrorString(e));
     return MQ_OK;
@@ -443,29 +270,39 @@ mq_status run_dequantize(const DequantArgs &a, cudaStream_t stream) {
     return MQ_OK;
 }
 
-// ---------------------------------------------------------------- scale order
-// One thread per (matrix, row tile, stage, unit, row): four scale bytes.
-__global__ void __launch_bounds__(256) fp4_scale_order_kernel(uint8_t *ordered, uint8_t *row_major,
-                                                              long long total, long long N, long long NT,
-                                                              int KS, int units, long long spitch,
-                                                              bool back) {
+// ---------------------------------------------------------------- order
+// Between row-major codes and scales and a weight's pieces: one thread for
+// every (piece, row, 16-byte unit), eight codes units and the row's scale
+// words by the unit's number.
+__global__ void __launch_bounds__(256) fp4_order_kernel(uint8_t *pieces, uint8_t *codes, uint8_t *scales,
+                                                        long long total, long long N, long long NT, int KS,
+                                                        int units, long long cpitch, long long spitch, bool back) {
+    const int piece_bytes = kFp4CodePiece + units * 512;
     for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<long long>(gridDim.x) * blockDim.x) {
-        const int row = static_cast<int>(i & 127);
-        long long k = i >> 7;  // unit within [E][NT][KS][units]
-        uint32_t *o = reinterpret_cast<uint32_t *>(ordered + k * 512 + (row & 31) * 16 + (row >> 5) * 4);
-        const int unit = static_cast<int>(k % units);
-        k /= units;
+        const int u = static_cast<int>(i & 7), row = static_cast<int>(i >> 3) & 127;
+        long long k = i >> 10;  // piece
+        uint8_t *piece = pieces + k * piece_bytes;
         const int ks = static_cast<int>(k % KS);
         k /= KS;
         const long long n = (k % NT) * 128 + row, e = k / NT;
-        const bool live = n < N;
-        uint32_t *s = reinterpret_cast<uint32_t *>(
-            row_major + (e * N + n) * spitch + (static_cast<long long>(ks) * units + unit) * 4);
-        if (back) {
-            if (live) *s = *o;
-        } else {
-            *o = live ? *s : 0u;
+        const long long col = static_cast<long long>(ks) * 128 + u * 16;
+        uint4 *at = reinterpret_cast<uint4 *>(piece + row * 128 + ((u ^ (row & 7)) * 16));
+        uint4 *from = reinterpret_cast<uint4 *>(codes + (e * N + n) * cpitch + col);
+        const bool live = n < N && col < cpitch;
+        if (!back)
+            *at = live ? *from : make_uint4(0, 0, 0, 0);
+        else if (live)
+            *from = *at;
+        if (u < units) {
+            const long long scol = (static_cast<long long>(ks) * units + u) * 4;
+            uint32_t *sat = reinterpret_cast<uint32_t *>(piece + kFp4CodePiece + u * 512 + (row & 31) * 16 + (row >> 5) * 4);
+            uint32_t *sfrom = reinterpret_cast<uint32_t *>(scales + (e * N + n) * spitch + scol);
+            const bool slive = n < N && scol < spitch;
+            if (!back)
+                *sat = slive ? *sfrom : 0u;
+            else if (slive)
+                *sfrom = *sat;
         }
     }
 }
@@ -477,9 +314,8 @@ mq_status launch_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64
                               uint8_t *scales, float *row_scale, cudaStream_t stream) {
     if (rows <= 0) return MQ_OK;
     const int64_t size = dtype == MQ_FP32 ? 4 : 2;
-    QuantArgs a{X, ldx, x_rows, index, codes, scales, row_scale, rows, K, fp4_code_pitch(K),
-                fp4_scale_pitch(fmt, K), static_cast<const char *>(X),
-                static_cast<const char *>(X) + ((x_rows - 1) * ldx + K) * size};
+    QuantArgs a{X, ldx, x_rows, index, codes, scales, row_scale, rows, fp4_code_pitch(K), fp4_scale_pitch(fmt, K),
+                {K, static_cast<const char *>(X), static_cast<const char *>(X) + ((x_rows - 1) * ldx + K) * size}};
     const bool nv = fmt == MQ_FP4_NV;
     switch (dtype) {
         case MQ_BF16: return nv ? pick_quantize<__nv_bfloat16, true>(a, stream) : pick_quantize<__nv_bfloat16, false>(a, stream);
@@ -503,16 +339,16 @@ mq_status launch_fp4_dequantize(const Fp4Rows &x, int64_t K, int fmt, void *Y, m
     return fail(MQ_ERR_INVALID_ARG, "unknown dtype");
 }
 
-mq_status launch_fp4_scale_order(const Fp4Device &d, uint8_t *row_major, bool to_row_major,
-                                 cudaStream_t stream) {
+mq_status launch_fp4_order(const Fp4Device &d, uint8_t *codes, uint8_t *scales, bool to_rows, cudaStream_t stream) {
     const int units = fp4_stage_scales(d.fmt) / 4;
-    const long long total = d.E * d.NT * d.KS * units * 128;
-    const long long blocks = std::min<long long>((total + 255) / 256, 16ll * sm_count());
-    fp4_scale_order_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        d.scales, row_major, total, d.N, d.NT, d.KS, units, fp4_scale_pitch(d.fmt, d.K), to_row_major);
+    const long long total = d.E * d.NT * d.KS * 1024;
+    const long long blocks = std::min<long long>((total + 255) / 256, 32ll * sm_count());
+    fp4_order_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+        d.pieces, codes, scales, total, d.N, d.NT, d.KS, units, fp4_code_pitch(d.K), fp4_scale_pitch(d.fmt, d.K),
+        to_rows);
     const cudaError_t e = cudaPeekAtLastError();
     if (e != cudaSuccess)
-        return fail(MQ_ERR_CUDA, std::string("fp4 scale order launch: ") + cudaGetErrorString(e));
+        return fail(MQ_ERR_CUDA, std::string("fp4 order launch: ") + cudaGetErrorString(e));
     return MQ_OK;
 }
 

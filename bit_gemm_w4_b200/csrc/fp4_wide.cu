@@ -13,10 +13,11 @@
 // Each CTA fills its own ring: warp 0 copies codes and weight scales (TMA),
 // warps 2 to 5 place all the tile's token scales (row-major in memory) in the
 // tensor core's order; both report to the first CTA's barriers, whose warp 1
-// issues scale copies to tensor memory and MMAs for the pair. Warps 6 to 9 are
-// the epilogue.
+// issues scale copies to tensor memory and MMAs for the pair. Warps 6 to 13
+// are the epilogue.
 
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "fp4.h"
@@ -26,16 +27,15 @@
 namespace mq {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
+constexpr int kStorers = 8;    // epilogue warps, two for each quarter of the lanes
 constexpr int kMaxStages = 8;
 constexpr int kBoxRows = 16;   // tokens of one copy in a tile that is not full
-constexpr int kATile = 128 * 128;
 constexpr int kMaxTT = 224;    // most tokens of a tile
 constexpr int kLoaders = 4, kLoadRows = (kMaxTT + 32 * kLoaders - 1) / (32 * kLoaders);
 
 struct WideParams {
-    CUtensorMap tw, tx, tx_small;  // boxes of 128 rows, TT / 2 tokens, 16 tokens
-    CUtensorMap tws;               // weight scales, one piece a box
+    CUtensorMap tw, tx, tx_small;  // boxes of a piece of the weight, TT / 2 tokens, 16 tokens
     const float *wfactor;
     const uint8_t *xscales;
     const float *xfactor;
@@ -58,9 +58,10 @@ struct WideSmem {
     static constexpr int kUnits = NV ? 4 : 2;
     static constexpr int kTT = NV ? 192 : kMaxTT;  // columns of one accumulator
     static constexpr uint32_t kScaleCols = 2 * kTT, kScaleSet = 12 * kUnits;
-    static constexpr int kA = kUnits * 512, kB = kUnits * 1024;  // scales: 128 rows, 256 tokens
-    __host__ __device__ static int slot(int TT) { return kATile + TT * 64 + kA + kB; }
-    __host__ __device__ static int total(int TT, int stages) { return slot(TT) * stages + 1024 + 256 + 4 * kMaxTT * 4; }
+    static constexpr int kPiece = kFp4CodePiece + kUnits * 512;
+    __host__ __device__ static int unit(int TT) { return TT > 128 ? 1024 : 512; }  // bytes of a unit of token scales
+    __host__ __device__ static int slot(int TT) { return kPiece + TT * 64 + kUnits * unit(TT); }
+    __host__ __device__ static int total(int TT, int stages) { return slot(TT) * stages + 1024 + 256 + kStorers * kMaxTT * 4; }
 };
 
 template <bool NV>
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                                                 ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int TT = p.TT, stages = p.stages, slot = S::slot(TT), KS = p.KS;
-    const int at_b = kATile, at_sa = kATile + TT * 64, at_sb = at_sa + S::kA;
+    const int at_b = S::kPiece, at_sb = at_b + TT * 64, unit = S::unit(TT);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + slot * stages);
     uint64_t *full = bars, *empty = bars + kMaxStages, *acc_full = bars + 2 * kMaxStages, *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);  // the epilogue warps of both CTAs
+            mbar_init(&acc_empty[b], 2 * kStorers);  // the epilogue warps of both CTAs
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -106,22 +107,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
         int s = 0, ph = 1, first = 1;
         bool ok = true;
         for (long long ti = pair; ok && walk.find(ti, t); ti += pairs) {
-            const int n0 = (t.nt * 2 + rank) * 128;
             const int n = (t.tokens + 31) / 32 * 32;  // the MMA's columns, unless the tile is full
             const bool whole = n >= TT;
             const int half = whole ? TT / 2 : n / 2;
-            const uint32_t bytes = 2 * (kATile + S::kA + half * 128);  // both CTAs' copies
-            // past the last row tile (an odd count) the codes read as zeros and the scales
-            // are another tile's: rows that are not stored
+            const uint32_t bytes = 2 * (S::kPiece + half * 128);  // both CTAs' copies
+            // past the last row tile (an odd count) that tile again: rows that are not stored
             const int nt1 = min(t.nt * 2 + static_cast<int>(rank), p.NT1 - 1);
             const int piece = (t.e * p.NT1 + nt1) * KS;
             const int mb = t.m0 + rank * half;
             auto weight = [&](int k, int slot_i) {
-                uint8_t *at = smem + slot_i * slot;
                 const uint32_t bar = in_cta(&full[slot_i], 0);
                 if (rank == 0) mbar_arrive_expect_tx(&full[slot_i], bytes);
-                tma_pair_load_3d(at, &p.tw, bar, k * 128, n0, t.e);
-                tma_pair_load_2d(at + at_sa, &p.tws, bar, 0, (piece + k) * (S::kA / 256));
+                tma_pair_load_2d(smem + slot_i * slot, &p.tw, bar, 0, (piece + k) * (S::kPiece / 128));
             };
             auto tokens_in = [&](int k, int slot_i) {
                 uint8_t *at = smem + slot_i * slot + at_b;
@@ -176,15 +173,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                 if (!ok) break;
                 tc5::fence_after();
                 const uint32_t at = smem_u32(smem) + s * slot;
-                const uint32_t sa = at + at_sa, sb = at + at_sb;
+                const uint32_t sa = at + kFp4CodePiece, sb = at + at_sb;
                 const uint32_t sfa = tmem + S::kScaleCols + set * S::kScaleSet, sfb = sfa + 4 * kUnits;
                 const uint64_t da = tc5::operand_desc(at), db = tc5::operand_desc(at + at_b);
                 if (tc5::elect()) {
 #pragma unroll
                     for (int u = 0; u < kUnits; ++u) {
                         tc5::copy_scales<2>(sfa + 4 * u, tc5::scale_desc(sa + 512 * u));
-                        tc5::copy_scales<2>(sfb + 8 * u, tc5::scale_desc(sb + 1024 * u));
-                        if (n > 128) tc5::copy_scales<2>(sfb + 8 * u + 4, tc5::scale_desc(sb + 1024 * u + 512));
+                        tc5::copy_scales<2>(sfb + 8 * u, tc5::scale_desc(sb + unit * u));
+                        if (n > 128) tc5::copy_scales<2>(sfb + 8 * u + 4, tc5::scale_desc(sb + unit * u + 512));
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -257,14 +254,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                         if (r < cur.tokens) {
                             uint32_t *dst = reinterpret_cast<uint32_t *>(at + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4);
                             const uint4 v = now[i][NV ? j : 0];
+                            const int next_unit = unit / 4;
                             if constexpr (NV) {
                                 dst[0] = v.x;
-                                dst[256] = v.y;
-                                dst[512] = v.z;
-                                dst[768] = v.w;
+                                dst[next_unit] = v.y;
+                                dst[2 * next_unit] = v.z;
+                                dst[3 * next_unit] = v.w;
                             } else {
                                 dst[0] = j ? v.z : v.x;
-                                dst[256] = j ? v.w : v.y;
+                                dst[next_unit] = j ? v.w : v.y;
                             }
                         }
                     }
@@ -277,12 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        // A warp stores 32 rows of the tile (its lanes) token by token. With
-        // even addresses two neighbouring lanes trade halves first, so that a
-        // store carries two rows of one token and a warp's store two tokens.
         pdl_wait();
-        const int quad = warp & 3, row = quad * 32 + lane;
-        float *factors = reinterpret_cast<float *>(smem + slot * stages + 256) + quad * kMaxTT;
+        const int quad = warp & 3, row = quad * 32 + lane, which = (warp - 6) >> 2;
+        float *factors = reinterpret_cast<float *>(smem + slot * stages + 256) + (warp - 6) * kMaxTT;
         int b = 0, bph = 0;
         for (long long ti = pair; walk.find(ti, t); ti += pairs) {
             const long long n = (t.nt * 2 + static_cast<int>(rank)) * 128ll + row;
@@ -290,27 +285,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
             const float fw = NV && live ? __ldg(p.wfactor + static_cast<long long>(t.e) * p.N + n) : 1.0f;
             if constexpr (NV) {
                 __syncwarp();
-                for (int m = lane; m < t.tokens; m += 32) factors[m] = p.xfactor[t.m0 + m];
+                for (int m = lane; m < t.tokens; m += 32) factors[m] = load_f32(p.xfactor + t.m0 + m);
                 __syncwarp();
             }
             if (!mbar_wait_warp(&acc_full[b], bph, p.err, kErrWaitMma, abort_flag)) break;
             tc5::fence_after();
             const uint32_t d = tmem + b * S::kTT + (static_cast<uint32_t>(quad) << 21);
+            // every other 16 tokens each, the next ones on their way meanwhile
             uint32_t next[16];
-            tc5::load16(d, next);
-            for (int c = 0; c < t.tokens; c += 16) {
+            int c = 16 * which;
+            if (c < t.tokens) tc5::load16(d + c, next);
+            for (; c < t.tokens; c += 32) {
                 float v[16];
                 tc5::load_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(next[j]);
-                if (c + 16 < t.tokens) {
-                    tc5::load16(d + c + 16, next);
-                } else {
-                    // the accumulator is read: the next tile but one may use it
-                    tc5::fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(in_cta(&acc_empty[b], 0));
-                }
+                if (c + 32 < t.tokens) tc5::load16(d + c + 32, next);
                 if constexpr (NV) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
@@ -321,32 +311,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                         v[j + 3] = v[j + 3] * f.w * fw;
                     }
                 }
-                const int left = t.tokens - c;
-                if (p.paired) {
-                    // even lanes store the chunk's even tokens, odd lanes its odd ones
-                    const int odd = lane & 1;
-                    uint32_t *y = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.Y) +
-                                                               (t.m0 + c + odd) * p.ldy + (n - odd));
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const uint32_t mine = p.fp16 ? pack_f16(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
-                        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                        const uint32_t w = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-                        if (live && j + odd < left) *y = w;
-                        y += p.ldy;  // two rows of 16-bit values
-                    }
-                } else if (live) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < left) store_output(p.Y, (t.m0 + c + j) * p.ldy + n, v[j], p.fp16);
-                }
+                store_chunk(v, p.Y, p.ldy, t.m0 + c, n, t.tokens - c, live, p.paired, p.fp16);
             }
+            // the accumulator is read: the next tile but one may use it
+            tc5::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(in_cta(&acc_empty[b], 0));
             if (++b == 2) b = 0, bph ^= 1;
         }
     }
     __syncwarp();
     drain_after_abort(abort_flag);
     __syncwarp();
+    pdl_wait();  // a launch is not over before the one it was chained to
     tc5::fence_before();
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may still reach it
@@ -370,10 +347,9 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     const int64_t tiles = (offsets ? std::min<int64_t>(d.E, x.rows) + x.rows / TT : (x.rows + TT - 1) / TT) * p.NT;
     p.stages = std::min(kMaxStages, (227 * 1024 - S::total(TT, 0)) / S::slot(TT));
     p.tw = d.map;
-    if (!encode_bytes_map(&p.tx, x.codes, d.pitch, x.rows, 0, TT / 2) ||
-        !encode_bytes_map(&p.tx_small, x.codes, d.pitch, x.rows, 0, kBoxRows))
+    if (!encode_bytes_map(&p.tx, x.codes, fp4_code_pitch(d.K), x.rows, TT / 2, true) ||
+        !encode_bytes_map(&p.tx_small, x.codes, fp4_code_pitch(d.K), x.rows, kBoxRows, true))
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activations");
-    p.tws = d.scale_map;
     p.paired = d.N % 2 == 0 && ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(Y) & 3) == 0;
     p.wfactor = d.row_scale;
     p.xscales = x.scales;
@@ -419,19 +395,23 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
 
 mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,
                           int64_t ldy, bool chained, cudaStream_t stream) {
-    // Tokens of a tile: the choice that leaves the least time over the waves
-    // of tiles, a tile's time growing with its tokens plus a share that does
-    // not depend on them.
-    const int64_t NT = (d.NT + 1) / 2, pairs = sm_count() / 2;
-    const int most = d.fmt == MQ_FP4_NV ? WideSmem<true>::kTT : WideSmem<false>::kTT;
-    int best = most;
-    if (!offsets) {
-        int64_t least = -1;
-        for (int TT = most; TT >= 64; TT -= 32) {
-            const int64_t tiles = (x.rows + TT - 1) / TT * NT;
-            const int64_t cost = (tiles + pairs - 1) / pairs * (TT + 64);
-            if (least < 0 || cost < least) least = cost, best = TT;
-        }
+    // Tokens of a tile: the choice that leaves the least time over the waves of
+    // tiles. A stage takes a time that does not depend on the tokens plus one
+    // for each of them, measured as 0.26 us + 0.46 ns a token (MQ_FP4_MX) and
+    // 0.31 us + 0.8 ns a token (MQ_FP4_NV, whose stages have twice the scales):
+    // 565 and 390 tokens' worth. Matrices of a ragged batch end half a tile
+    // early on average.
+    const bool nv = d.fmt == MQ_FP4_NV;
+    const int64_t NT = (d.NT + 1) / 2, pairs = sm_count() / 2, mats = std::min<int64_t>(d.E, x.rows);
+    int best = 0;
+    double least = 0;
+    for (int TT = nv ? WideSmem<true>::kTT : WideSmem<false>::kTT; TT >= 32; TT -= 32) {
+        const double even = static_cast<double>((x.rows + mats * TT - 1) / (mats * TT)) * mats;
+        const double tiles = (mats == 1 ? even : std::max<double>(mats, static_cast<double>(x.rows) / TT + 0.5 * mats)) * NT;
+        double waves = tiles / pairs;
+        if (mats == 1 || waves < 1) waves = std::ceil(waves);
+        const double cost = waves * (TT + (nv ? 390 : 565));
+        if (!best || cost < least) least = cost, best = TT;
     }
     return d.fmt == MQ_FP4_NV ? run_wide<true>(d, x, offsets, Y, dtype, ldy, chained, stream, best)
                               : run_wide<false>(d, x, offsets, Y, dtype, ldy, chained, stream, best);

@@ -703,10 +703,13 @@ class Fp4Weight:
     def _workspace(self, workspace, rows: int):
         if workspace is None:
             n = _lib.mq_fp4_workspace_bytes(self._h, rows)
-            return _t.empty(n, dtype=_t.u8, device=self.device), n
+            if not n:
+                return None, None, 0
+            workspace = _t.empty(n, dtype=_t.u8, device=self.device)
+            return workspace, workspace.data_ptr(), n
         if workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
-        return workspace, workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
     def _quantized(self, X: Fp4Tensor, dtype):
         if X.fmt != self.fmt or X.K != self.K or X.codes.get_device() != self._index:
@@ -739,8 +742,8 @@ class Fp4Weight:
             return Y
         d, X, M, _, ldx = self._input(X, dtype)
         Y, ldy = self._output(Y, M, X.dtype)
-        workspace, nbytes = self._workspace(workspace, M)
-        st = _lib.mq_fp4_linear(self._h, X.data_ptr(), d, M, ldx, Y.data_ptr(), ldy, workspace.data_ptr(), nbytes,
+        workspace, at_ws, nbytes = self._workspace(workspace, M)
+        st = _lib.mq_fp4_linear(self._h, X.data_ptr(), d, M, ldx, Y.data_ptr(), ldy, at_ws, nbytes,
                                 _t.raw_stream(index))
         if st:
             _check(st, "mq_fp4_linear")
@@ -775,9 +778,9 @@ class Fp4Weight:
             rows = _index(rows, index, "rows")
             R, at = rows.shape[0], rows.data_ptr()
         Y, ldy = self._output(Y, R, X.dtype)
-        workspace, nbytes = self._workspace(workspace, R)
+        workspace, at_ws, nbytes = self._workspace(workspace, R)
         st = _lib.mq_fp4_linear_grouped(self._h, X.data_ptr(), d, M, ldx, at, R, offsets.data_ptr(), Y.data_ptr(), ldy,
-                                        workspace.data_ptr(), nbytes, _t.raw_stream(index))
+                                        at_ws, nbytes, _t.raw_stream(index))
         if st:
             _check(st, "mq_fp4_linear_grouped")
         return Y

@@ -336,9 +336,10 @@ def test_grouped_bad_offsets_stay_inside(mq, cuda, fmt, offsets):
 def test_refusals(mq, cuda):
     w1 = mq.Fp4Weight.pack(values(64, 64, BF16, 1).to(cuda), "nvfp4")
     w2 = mq.Fp4Weight.pack(values(128, 64, BF16, 1).view(2, 64, 64).to(cuda), "nvfp4")
-    X = values(4, 64, BF16, 2).to(cuda)
-    off = torch.tensor([0, 1, 4], dtype=torch.int32, device=cuda)
-    Y = torch.empty(4, 64, dtype=BF16, device=cuda)
+    M = 40  # enough that the product needs its workspace
+    X = values(M, 64, BF16, 2).to(cuda)
+    off = torch.tensor([0, 1, M], dtype=torch.int32, device=cuda)
+    Y = torch.empty(M, 64, dtype=BF16, device=cuda)
     with pytest.raises(mq.MQError):
         w2.linear(X)                               # several matrices
     for call in (lambda: w1.linear(X.float()), lambda: w1.linear(X[:, :63]), lambda: w1.linear(X.cpu()),
@@ -350,15 +351,15 @@ def test_refusals(mq, cuda):
                  lambda: w2.linear_grouped(mq.fp4_quantize(X), off, rows=off)):
         with pytest.raises(ValueError):
             call()
-    small = torch.empty(w1.workspace_bytes(4) - 16, dtype=torch.uint8, device=cuda)
+    small = torch.empty(w1.workspace_bytes(M) - 16, dtype=torch.uint8, device=cuda)
     with pytest.raises(mq.MQError):
         w1.linear(X, Y, small)
     with pytest.raises(mq.MQError):
-        w1.linear(X, Y, torch.empty(w1.workspace_bytes(4) + 16, dtype=torch.uint8, device=cuda)[1:])
+        w1.linear(X, Y, torch.empty(w1.workspace_bytes(M) + 16, dtype=torch.uint8, device=cuda)[1:])
     lib = mq.lib()
     s = torch.cuda.current_stream().cuda_stream
-    ws = torch.empty(w2.workspace_bytes(4), dtype=torch.uint8, device=cuda)
-    args = [w2.handle, X.data_ptr(), 0, 4, 64, None, 4, off.data_ptr(), Y.data_ptr(), 64, ws.data_ptr(), ws.numel(), s]
+    ws = torch.empty(w2.workspace_bytes(M), dtype=torch.uint8, device=cuda)
+    args = [w2.handle, X.data_ptr(), 0, M, 64, None, M, off.data_ptr(), Y.data_ptr(), 64, ws.data_ptr(), ws.numel(), s]
     for k, bad, status in ((2, 2, 2), (4, 63, 1), (6, 3, 1), (7, None, 1), (7, off.data_ptr() + 1, 1), (8, None, 1),
                            (8, Y.data_ptr() + 1, 1), (9, 63, 1), (10, None, 1), (11, ws.numel() - 1, 1)):
         a = list(args)
@@ -406,7 +407,7 @@ def test_graphs_that_share_a_workspace(mq, cuda, fmt, T):
     E, N, K = 4, 200, 320
     w = mq.Fp4Weight.pack(values(E * N, K, BF16, 1).view(E, N, K).to(cuda), fmt)
     lin = mq.Fp4Weight.pack(values(N, K, BF16, 3).to(cuda), fmt)
-    ws = torch.empty(max(w.workspace_bytes(T), lin.workspace_bytes(T)), dtype=torch.uint8, device=cuda)
+    ws = torch.empty(max(16, w.workspace_bytes(T), lin.workspace_bytes(T)), dtype=torch.uint8, device=cuda)
     X = values(T, K, BF16, 4).to(cuda)
     offsets = torch.tensor([0, 0, T, T, T], dtype=torch.int32, device=cuda)
     Y = [torch.zeros(T, N, dtype=BF16, device=cuda) for _ in range(2)]
