@@ -20,6 +20,12 @@ struct RowSource {
 };
 
 // ---------------------------------------------------------------- conversions
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+
 // Eight values to eight E2M1 codes, the first in the low nibble; rounded to
 // nearest even, saturating at 6.
 __device__ __forceinline__ uint32_t e2m1_x8(const float *v) {
@@ -35,16 +41,12 @@ __device__ __forceinline__ uint32_t e2m1_x8(const float *v) {
     return d;
 }
 
-// Eight E2M1 codes to their values as four f16x2 (exact).
-__device__ __forceinline__ void e2m1_values(uint32_t codes, uint32_t (&h)[4]) {
-    asm("{\n\t.reg .b8 a, b, c, e;\n\t"
-        "mov.b32 {a, b, c, e}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, e;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(codes));
+// The two E2M1 codes of a byte (the low eight bits) to their values as f16x2
+// (exact).
+__device__ __forceinline__ uint32_t e2m1_values(uint32_t byte) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 a;\n\tcvt.u8.u32 a, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(byte));
+    return h;
 }
 
 __device__ __forceinline__ uint32_t e4m3_bits(float v) {
@@ -76,13 +78,13 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
-    // The largest magnitude's bits; an order of non-negative floats is the
-    // order of their bits, infinities and NaN above every finite value.
+    // The largest magnitude's bits, a NaN's where there is one (the order of
+    // non-negative floats is the order of their bits).
     __device__ __forceinline__ uint32_t max_bits() const {
         if constexpr (sizeof(T) == 2) {
-            uint32_t m = 0;
+            uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+            for (int i = 1; i < kWords; ++i) m = max_abs2(m, w[i]);
             return max(m & 0xFFFFu, m >> 16);
         } else {
             uint32_t m = 0;
@@ -90,6 +92,15 @@ struct Raw {
             for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
             return m;
         }
+    }
+    // max(m, |v|) of two 16-bit elements, NaN if either is.
+    static __device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t v) {
+        uint32_t d;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(d) : "r"(m), "r"(v));
+        else
+            asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %2;\n\tmax.NaN.f16x2 %0, %1, a;\n\t}" : "=r"(d) : "r"(m), "r"(v));
+        return d;
     }
     __device__ __forceinline__ float value(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
@@ -182,6 +193,17 @@ __device__ __forceinline__ void load_chunk(Raw<T> &r, const RowSource &a, const 
     }
 }
 
+// The same for a whole chunk on a 32-byte boundary.
+template <class T>
+__device__ __forceinline__ void load_whole_chunk(Raw<T> &r, const T *p) {
+#pragma unroll
+    for (int i = 0; i < Raw<T>::kWords / 8; ++i)
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r.w[8 * i]), "=r"(r.w[8 * i + 1]), "=r"(r.w[8 * i + 2]), "=r"(r.w[8 * i + 3]),
+                       "=r"(r.w[8 * i + 4]), "=r"(r.w[8 * i + 5]), "=r"(r.w[8 * i + 6]), "=r"(r.w[8 * i + 7])
+                     : "l"(p + i * (32 / sizeof(T))));
+}
+
 // ---------------------------------------------------------------- decisions
 // All in 32 bits, one rounding an operation, in the order the header states.
 
@@ -214,14 +236,21 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t top_bits, float &inv) {
     return finite ? s : 255u;
 }
 
-// Sixteen codes, the first in the low nibble.
+// Sixteen codes, the first in the low nibble; zeros where inv is 0 (which
+// also keeps what an infinity or a NaN times 0 gives out).
 template <class T>
 __device__ __forceinline__ uint2 codes_of(const Raw<T> &raw, float inv) {
     float v[kChunk];
-    const bool zero = inv == 0.0f;  // also keeps infinities times 0 out
+    const uint64_t i2 = pack2(inv, inv);
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) v[k] = zero ? 0.0f : __fmul_rn(raw.value(k), inv);
-    return make_uint2(e2m1_x8(v), e2m1_x8(v + 8));
+    for (int k = 0; k < kChunk; k += 2) {
+        uint64_t d;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(raw.value(k), raw.value(k + 1))), "l"(i2));
+        v[k] = __uint_as_float(static_cast<uint32_t>(d));
+        v[k + 1] = __uint_as_float(static_cast<uint32_t>(d >> 32));
+    }
+    const uint32_t keep = inv == 0.0f ? 0u : 0xFFFFFFFFu;
+    return make_uint2(e2m1_x8(v) & keep, e2m1_x8(v + 8) & keep);
 }
 
 }  // namespace mq

@@ -31,125 +31,98 @@ struct QuantArgs {
 };
 
 // ---------------------------------------------------------------- quantise
-// blockDim = (bx, by): bx threads share a row, by rows side by side, kRows
-// rows one after another in each thread's registers (their loads are issued
-// together). A thread holds kChunks chunks of a row; wider rows are read
-// twice by MQ_FP4_NV, whose row factor needs the whole row first.
-template <class T, bool NV, int kChunks, int kRows>
+// blockDim = (bx, by): bx threads share a row, by rows side by side. A thread
+// holds kChunks chunks of its row, all on their way from memory at once;
+// wider rows are read twice by MQ_FP4_NV, whose row factor needs the whole row
+// first.
+template <class T, bool NV, int kChunks>
 __global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
     // The launch after this one may start once the launches before are over.
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int kMaxWarps = 32;
-    __shared__ uint32_t wmax[NV ? kRows * kMaxWarps : 1];
+    __shared__ uint32_t wmax[16];
     const int bx = blockDim.x, tx = threadIdx.x, ty = threadIdx.y;
-    const long long chunks = NV ? a.spitch : a.spitch * 2;  // the scales' padding included
-    const long long step = static_cast<long long>(bx) * kChunks;
-    const long long r0 = (static_cast<long long>(blockIdx.x) * blockDim.y + ty) * kRows;
-
-    const T *src[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const long long r = r0 + i;
-        src[i] = nullptr;
-        if (r < a.rows) {
-            const long long x = a.index ? static_cast<long long>(load_i32(a.index + r)) : r;
-            if (x >= 0 && x < a.x_rows) src[i] = static_cast<const T *>(a.X) + x * a.ldx;
-        }
+    const int chunks = static_cast<int>(NV ? a.spitch : a.spitch * 2);  // the scales' padding included
+    const int code_chunks = static_cast<int>(a.cpitch / 8), real_chunks = static_cast<int>((a.from.K + kChunk - 1) / kChunk);
+    const int whole_chunks = static_cast<int>(a.from.K / kChunk);
+    const int step = bx * kChunks;
+    const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + ty;
+    const bool real = r < a.rows;
+    const T *src = nullptr;
+    if (real) {
+        const long long x = a.index ? static_cast<long long>(load_i32(a.index + r)) : r;
+        if (x >= 0 && x < a.x_rows) src = static_cast<const T *>(a.X) + x * a.ldx;
     }
-    Raw<T> raw[kRows][kChunks];
-    auto load = [&](long long base) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(src) & 31) == 0;
+    auto load_one = [&](Raw<T> &t, int ch) {
+        if (src && aligned && ch < whole_chunks)
+            load_whole_chunk(t, src + ch * kChunk);
+        else if (src && ch < real_chunks)
+            load_chunk(t, a.from, src, static_cast<long long>(ch) * kChunk);
+        else
+            t.clear();
+    };
+    Raw<T> raw[kChunks];
+    auto load = [&](int base) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-            for (int j = 0; j < kChunks; ++j) {
-                const long long c = (base + tx + static_cast<long long>(j) * bx) * kChunk;
-                if (src[i])
-                    load_chunk(raw[i][j], a.from, src[i], c);
-                else
-                    raw[i][j].clear();
-            }
+        for (int j = 0; j < kChunks; ++j) load_one(raw[j], base + tx + j * bx);
     };
     load(0);
 
-    float factor[kRows], inv_factor[kRows];
+    float factor = 0.0f, inverse = 0.0f;
     if constexpr (NV) {
-        uint32_t m[kRows];
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            m[i] = 0;
-#pragma unroll
-            for (int j = 0; j < kChunks; ++j) m[i] = max(m[i], raw[i][j].max_bits());
-        }
-        for (long long base = step; base < chunks; base += step) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                for (int j = 0; j < kChunks; ++j) {
-                    Raw<T> t;
-                    if (src[i])
-                        load_chunk(t, a.from, src[i], (base + tx + static_cast<long long>(j) * bx) * kChunk);
-                    else
-                        t.clear();
-                    m[i] = max(m[i], t.max_bits());
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) m[i] = __reduce_max_sync(0xffffffffu, m[i]);
-        if (bx > 32) {
-            const int warps = bx >> 5, w0 = ty * warps;
-            if ((tx & 31) == 0)
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) wmax[i * kMaxWarps + w0 + (tx >> 5)] = m[i];
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int l = tx & 31;
-                m[i] = __reduce_max_sync(0xffffffffu, l < warps ? wmax[i * kMaxWarps + w0 + l] : 0u);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            factor[i] = nv_factor<T>(m[i], inv_factor[i]);
-            if (tx == 0 && r0 + i < a.rows) a.row_scale[r0 + i] = factor[i];
-        }
-    }
-
-    for (long long base = 0; base < chunks; base += step) {
-        if (base > 0) load(base);
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const long long r = r0 + i;
+        for (int j = 0; j < kChunks; ++j) m = max(m, raw[j].max_bits());
+        for (int base = step; base < chunks; base += step) {
 #pragma unroll
             for (int j = 0; j < kChunks; ++j) {
-                const long long ch = base + tx + static_cast<long long>(j) * bx;
-                uint32_t top = raw[i][j].max_bits();
-                float inv;
-                uint32_t sbits;
-                if constexpr (NV) {
-                    sbits = nv_scale<T>(top, factor[i], inv_factor[i], inv);
-                } else {
-                    // lanes 2i and 2i + 1 hold the two halves of a block
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    sbits = mx_scale<T>(top, inv);
-                }
-                if (r >= a.rows || ch >= chunks) continue;
-                if (ch * 8 < a.cpitch)
-                    *reinterpret_cast<uint2 *>(a.codes + r * a.cpitch + ch * 8) = codes_of(raw[i][j], inv);
-                if (ch * kChunk >= a.from.K) sbits = 0;
-                if constexpr (NV)
-                    a.scales[r * a.spitch + ch] = static_cast<uint8_t>(sbits);
-                else if ((ch & 1) == 0)
-                    a.scales[r * a.spitch + (ch >> 1)] = static_cast<uint8_t>(sbits);
+                Raw<T> t;
+                load_one(t, base + tx + j * bx);
+                m = max(m, t.max_bits());
             }
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (bx > 32) {
+            const int warps = bx >> 5, lane = tx & 31;
+            if (lane == 0) wmax[ty * warps + (tx >> 5)] = m;
+            __syncthreads();
+            m = __reduce_max_sync(0xffffffffu, lane < warps ? wmax[ty * warps + lane] : 0u);
+        }
+        factor = nv_factor<T>(m, inverse);
+        if (tx == 0 && real) a.row_scale[r] = factor;
+    }
+
+    uint8_t *codes = a.codes + r * a.cpitch, *scales = a.scales + r * a.spitch;
+    for (int base = 0; base < chunks; base += step) {
+        if (base > 0) load(base);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int ch = base + tx + j * bx;
+            uint32_t top = raw[j].max_bits(), scale;
+            float inv;
+            if constexpr (NV) {
+                scale = nv_scale<T>(top, factor, inverse, inv);
+            } else {
+                // lanes 2i and 2i + 1 hold the two halves of a block
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                scale = mx_scale<T>(top, inv);
+            }
+            if (!real || ch >= chunks) continue;
+            if (ch < code_chunks) *reinterpret_cast<uint2 *>(codes + ch * 8) = codes_of(raw[j], inv);
+            if (ch >= real_chunks) scale = 0;
+            if constexpr (NV)
+                scales[ch] = static_cast<uint8_t>(scale);
+            else if ((ch & 1) == 0)
+                scales[ch >> 1] = static_cast<uint8_t>(scale);
         }
     }
 }
 
-template <class T, bool NV, int kChunks, int kRows>
-mq_status run_quantize(const QuantArgs &a, int bx, int by, cudaStream_t stream) {
-    const long long per = static_cast<long long>(by) * kRows;
-    const long long grid = (a.rows + per - 1) / per;
+template <class T, bool NV, int kChunks>
+mq_status run_quantize(const QuantArgs &a, int bx, cudaStream_t stream) {
+    const int by = std::max(1, 128 / bx);
+    const long long grid = (a.rows + by - 1) / by;
     if (grid > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 quantisation: too many rows");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -160,7 +133,7 @@ mq_status run_quantize(const QuantArgs &a, int bx, int by, cudaStream_t stream) 
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, NV, kChunks, kRows>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, NV, kChunks>, a);
     if (e != cudaSuccess)
         return fail(MQ_ERR_CUDA, std::string("fp4 quantisation launch: ") + cudaGetErrorString(e));
     return MQ_OK;
@@ -169,23 +142,15 @@ mq_status run_quantize(const QuantArgs &a, int bx, int by, cudaStream_t stream) 
 template <class T, bool NV>
 mq_status pick_quantize(const QuantArgs &a, cudaStream_t stream) {
     const long long chunks = NV ? a.spitch : a.spitch * 2;
-    int bx = 32;
-    while (bx < 128 && bx < chunks) bx *= 2;
-    const int by = 256 / std::max(bx, 128) * (bx < 128 ? 128 / bx : 1);
-    if (chunks <= 128) return run_quantize<T, NV, 1, 1>(a, bx, by, stream);
     auto threads = [&](int per) {
-        const long long n = (chunks + per - 1) / per;
-        return static_cast<int>(std::min<long long>(512, (n + 31) / 32 * 32));
+        return static_cast<int>(std::min<long long>(512, ((chunks + per - 1) / per + 31) / 32 * 32));
     };
-    if (chunks <= 512) {
-        if (a.rows >= 4ll * 4 * sm_count()) return run_quantize<T, NV, 1, 4>(a, threads(1), 1, stream);
-        return run_quantize<T, NV, 1, 1>(a, threads(1), 1, stream);
-    }
-    if (chunks <= 1024) {
-        if (a.rows >= 4ll * 2 * sm_count()) return run_quantize<T, NV, 2, 2>(a, threads(2), 1, stream);
-        return run_quantize<T, NV, 2, 1>(a, threads(2), 1, stream);
-    }
-    return run_quantize<T, NV, 4, 1>(a, threads(4), 1, stream);
+    // Few rows: spread over threads, for the shortest way from load to store.
+    // Many: as many chunks a thread as a row has for a warp, up to four.
+    if (chunks <= 32 || (a.rows * chunks <= 512ll * sm_count() && chunks <= 512))
+        return run_quantize<T, NV, 1>(a, threads(1), stream);
+    if (chunks <= 64) return run_quantize<T, NV, 2>(a, 32, stream);
+    return run_quantize<T, NV, 4>(a, threads(4), stream);
 }
 
 // ---------------------------------------------------------------- dequantise
@@ -198,56 +163,118 @@ struct DequantArgs {
 
 // A thread writes aligned 16-byte units of Y, whatever the row's start: the
 // unit's columns are any run of 8 (16-bit types) or 4 (fp32), whose codes
-// come out of two words and whose scales are at most two.
+// come out of two words and whose scales are at most two. Four units a thread
+// (a block's width apart) are on their way at once.
 template <class T, bool NV>
 __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const DequantArgs a) {
     constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
-    constexpr int kBlock = NV ? 16 : 32;
+    constexpr int kShift = NV ? 4 : 5;  // log2 of the columns of a block
+    constexpr int kUnits = 4;
     const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (r >= a.rows) return;
     T *row = static_cast<T *>(a.Y) + r * a.ldy;
     const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     const uint32_t *words = reinterpret_cast<const uint32_t *>(a.codes + r * a.cpitch);
-    const long long nwords = a.cpitch / 4;
+    const int nwords = static_cast<int>(a.cpitch / 4), K = static_cast<int>(a.K);
     const uint8_t *sc = a.scales + r * a.spitch;
     const float factor = NV ? __ldg(a.row_scale + r) : 1.0f;
-    const long long units = (a.K + lead + kUnit - 1) / kUnit;
-    auto scale = [&](long long b) {
-        const uint32_t s = __ldg(sc + b);
-        return NV ? e4m3_value(s) : e8m0_value(s);
+    const int units = (K + lead + kUnit - 1) / kUnit;
+    const int u0 = blockIdx.y * (blockDim.x * kUnits) + threadIdx.x;
+    // Two codes' values as fp32 pairs: exact in f16, the products with an e4m3
+    // scale too (6 of 11 bits), so that only the row's factor rounds.
+    auto pair = [&](uint32_t byte, uint32_t scale_f16x2, float scale) {
+        uint32_t h = e2m1_values(byte);
+        if constexpr (NV) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(scale_f16x2));
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        uint64_t d;
+        const float f = NV ? factor : scale;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(v.x, v.y)), "l"(pack2(f, f)));
+        return make_float2(__uint_as_float(static_cast<uint32_t>(d)), __uint_as_float(static_cast<uint32_t>(d >> 32)));
     };
-    for (long long u = static_cast<long long>(blockIdx.y) * blockDim.x + threadIdx.x; u < units;
-         u += static_cast<long long>(gridDim.y) * blockDim.x) {
-        const long long c0 = u * kUnit - lead;  // negative in the first unit of a row with a lead
-        const long long w = c0 >> 3;
-        const int sh = static_cast<int>(c0 & 7) * 4;
+    auto twice = [](uint32_t s) {  // an e4m3 scale as f16x2
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(s | s << 8)));
+        return h;
+    };
+    if (lead == 0) {
+        uint32_t code[kUnits], scale[kUnits];
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = min(u0 + i * static_cast<int>(blockDim.x), units - 1);
+            const uint32_t w = __ldg(words + u / (8 / kUnit));
+            code[i] = kUnit == 8 ? w : w >> (16 * (u & 1));
+            scale[i] = __ldg(sc + ((u * kUnit) >> kShift));
+        }
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = u0 + i * static_cast<int>(blockDim.x);
+            if (u >= units) break;
+            const uint32_t s2 = NV ? twice(scale[i]) : 0u;
+            const float s = NV ? 0.0f : e8m0_value(scale[i]);
+            uint32_t out[4];
+#pragma unroll
+            for (int k = 0; k < kUnit / 2; ++k) {
+                const float2 v = pair(code[i] >> (8 * k), s2, s);
+                if constexpr (std::is_same<T, float>::value) {
+                    out[2 * k] = __float_as_uint(v.x);
+                    out[2 * k + 1] = __float_as_uint(v.y);
+                } else {
+                    out[k] = std::is_same<T, __half>::value ? pack_f16(v.x, v.y) : pack_bf16(v.x, v.y);
+                }
+            }
+            if ((u + 1) * kUnit <= K) {
+                *reinterpret_cast<uint4 *>(row + u * kUnit) = make_uint4(out[0], out[1], out[2], out[3]);
+            } else {
+                const T *o = reinterpret_cast<const T *>(out);
+#pragma unroll
+                for (int k = 0; k < kUnit; ++k)
+                    if (u * kUnit + k < K) row[u * kUnit + k] = o[k];
+            }
+        }
+        return;
+    }
+    uint32_t code[kUnits], s0[kUnits], s1[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const int u = min(u0 + i * static_cast<int>(blockDim.x), units - 1);
+        const int c0 = u * kUnit - lead;  // negative in the first unit of a row with a lead
+        const int w = c0 >> 3, sh = (c0 & 7) * 4;
         const uint32_t lo = w >= 0 ? __ldg(words + w) : 0u;
         const uint32_t hi = sh && w + 1 < nwords ? __ldg(words + w + 1) : 0u;
-        uint32_t h[4];
-        e2m1_values(__funnelshift_r(lo, hi, sh), h);
-        const long long first = max(c0, 0ll), last = min(c0 + kUnit, a.K) - 1;
-        const long long b0 = first / kBlock, b1 = last / kBlock;
-        const float s0 = scale(b0), s1 = b1 != b0 ? scale(b1) : s0;
-        T out[kUnit];
+        code[i] = __funnelshift_r(lo, hi, sh);
+        s0[i] = __ldg(sc + (max(c0, 0) >> kShift));
+        s1[i] = __ldg(sc + ((min(c0 + kUnit, K) - 1) >> kShift));
+    }
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-            const __half2 p = *reinterpret_cast<const __half2 *>(&h[i >> 1]);
-            float v = i & 1 ? __high2float(p) : __low2float(p);
-            v = __fmul_rn(v, (c0 + i) / kBlock > b0 ? s1 : s0);
-            if constexpr (NV) v = __fmul_rn(v, factor);
-            if constexpr (std::is_same<T, float>::value)
-                out[i] = v;
-            else if constexpr (std::is_same<T, __half>::value)
-                out[i] = __float2half_rn(v);
-            else
-                out[i] = __float2bfloat16_rn(v);
+    for (int i = 0; i < kUnits; ++i) {
+        const int u = u0 + i * static_cast<int>(blockDim.x);
+        if (u >= units) break;
+        const int c0 = u * kUnit - lead;
+        // the second scale begins at this of the unit's columns, if at all
+        const int edge = ((((max(c0, 0)) >> kShift) + 1) << kShift) - c0;
+        const uint32_t a2 = NV ? twice(s0[i]) : 0u, b2 = NV ? twice(s1[i]) : 0u;
+        const float af = NV ? 0.0f : e8m0_value(s0[i]), bf = NV ? 0.0f : e8m0_value(s1[i]);
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < kUnit / 2; ++k) {
+            const uint32_t byte = code[i] >> (8 * k);
+            // an odd lead lets the edge fall between the two
+            float2 v = pair(byte, 2 * k < edge ? a2 : b2, 2 * k < edge ? af : bf);
+            if (2 * k + 1 == edge) v.y = pair(byte, b2, bf).y;
+            if constexpr (std::is_same<T, float>::value) {
+                out[2 * k] = __float_as_uint(v.x);
+                out[2 * k + 1] = __float_as_uint(v.y);
+            } else {
+                out[k] = std::is_same<T, __half>::value ? pack_f16(v.x, v.y) : pack_bf16(v.x, v.y);
+            }
         }
-        if (c0 >= 0 && c0 + kUnit <= a.K) {
-            *reinterpret_cast<uint4 *>(row + c0) = *reinterpret_cast<const uint4 *>(out);
+        if (c0 >= 0 && c0 + kUnit <= K) {
+            *reinterpret_cast<uint4 *>(row + c0) = make_uint4(out[0], out[1], out[2], out[3]);
         } else {
+            const T *o = reinterpret_cast<const T *>(out);
 #pragma unroll
-            for (int i = 0; i < kUnit; ++i)
-                if (c0 + i >= 0 && c0 + i < a.K) row[c0 + i] = out[i];
+            for (int k = 0; k < kUnit; ++k)
+                if (c0 + k >= 0 && c0 + k < K) row[c0 + k] = o[k];
         }
     }
 }
@@ -256,12 +283,10 @@ template <class T, bool NV>
 mq_status run_dequantize(const DequantArgs &a, cudaStream_t stream) {
     const long long units = (a.K * static_cast<long long>(sizeof(T)) + 15) / 16 + 1;
     int bx = 32;
-    while (bx < 256 && bx < units) bx *= 2;
+    while (bx < 256 && bx * 4 < units) bx *= 2;
     const int by = 256 / bx;
-    const long long gx = (a.rows + by - 1) / by;
-    // two units a thread, so that short rows and few rows still spread out
-    const long long gy = std::max<long long>(1, std::min<long long>(64, units / (2 * bx)));
-    if (gx > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 dequantisation: too many rows");
+    const long long gx = (a.rows + by - 1) / by, gy = (units + bx * 4 - 1) / (bx * 4);
+    if (gx > 0x7FFFFFFFll || gy > 65535) return fail(MQ_ERR_UNSUPPORTED, "fp4 dequantisation: too large");
     fp4_dequantize_kernel<T, NV><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(bx, by), 0,
                                    stream>>>(a);
     const cudaError_t e = cudaPeekAtLastError();
