@@ -31,6 +31,16 @@ __device__ __forceinline__ float load_f32(const float *p) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t load_word(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_byte(const uint8_t *p) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .u8 b;\n\tld.global.nc.u8 b, [%1];\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(v) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ uint4 load_u128(const void *p) {
     uint4 v;
     asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -120,43 +130,54 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Sixteen tokens' outputs of this lane's weight row n (v; `left` of them are
-// real, `live`: n < N) into Y [tokens][ldy], whose first token is m. With
-// `paired` (N, ldy and Y's address even) neighbouring lanes trade halves
-// first: even lanes store two rows of the even tokens, odd lanes two rows of
-// the odd ones, 4 bytes a lane and two tokens a warp's store. Called by whole
-// warps.
-__device__ __forceinline__ void store_chunk(const float (&v)[16], void *Y, long long ldy, long long m, long long n,
-                                            int left, bool live, bool paired, bool fp16) {
-    if (paired) {
-        const int odd = threadIdx.x & 1;
-        uint32_t w[8];
+// Sixteen tokens' outputs of this lane's weight row, as 16-bit words ready to
+// be stored. With `paired` (N, ldy and Y's address even) neighbouring lanes
+// trade halves: even lanes then hold two rows of the even tokens, odd lanes
+// two rows of the odd ones, 4 bytes a lane and two tokens a warp's store;
+// without, a word holds two tokens of the lane's own row. Called by whole warps.
+__device__ __forceinline__ void pack_chunk(const float (&v)[16], uint32_t (&w)[8], bool paired, bool fp16) {
+    const bool odd = threadIdx.x & 1;
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const uint32_t mine = fp16 ? pack_f16(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
+    for (int j = 0; j < 16; j += 2) {
+        const uint32_t mine = fp16 ? pack_f16(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
+        w[j / 2] = mine;
+        if (paired) {
             const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
             w[j / 2] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
         }
+    }
+}
+
+// pack_chunk's words into Y [tokens][ldy]: tokens m .. m + 15, of which `left`
+// are real, for row n (live: n < N).
+__device__ __forceinline__ void store_packed(const uint32_t (&w)[8], void *Y, long long ldy, long long m, long long n,
+                                             int left, bool live, bool paired) {
+    if (!live) return;
+    if (paired) {
+        const int odd = threadIdx.x & 1;
         // ldy words of 4 bytes: two rows of 16-bit values
         uint32_t *y = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(Y) + (m + odd) * ldy + (n - odd));
         if (left >= 16) {
-            if (live) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j, y += ldy) *y = w[j];
-            }
+            for (int j = 0; j < 8; ++j, y += ldy) *y = w[j];
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j, y += ldy)
-                if (live && 2 * j + odd < left) *y = w[j];
+                if (2 * j + odd < left) *y = w[j];
         }
         return;
     }
     uint16_t *y = static_cast<uint16_t *>(Y) + m * ldy + n;
 #pragma unroll
-    for (int j = 0; j < 16; ++j, y += ldy) {
-        const uint32_t b = fp16 ? pack_f16(v[j], 0.0f) : pack_bf16(v[j], 0.0f);
-        if (live && j < left) *y = static_cast<uint16_t>(b);
-    }
+    for (int j = 0; j < 16; ++j, y += ldy)
+        if (j < left) *y = static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+}
+
+__device__ __forceinline__ void store_chunk(const float (&v)[16], void *Y, long long ldy, long long m, long long n,
+                                            int left, bool live, bool paired, bool fp16) {
+    uint32_t w[8];
+    pack_chunk(v, w, paired, fp16);
+    store_packed(w, Y, ldy, m, n, left, live, paired);
 }
 
 // Bulk copy of `bytes` (a multiple of 16) into shared memory, completing on `bar`.

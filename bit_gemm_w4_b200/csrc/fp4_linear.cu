@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
         const uint32_t desc = tc5::idesc(128, nb * kBoxRows, !NV);
         const uint32_t sfa = tmem + TT, sfb = sfa + 4 * kUnits;
         bool ok = true;
+        pdl_wait();  // before any wait with a limit: the launch before may take its time
         for (int i = 0, s = 0, ph = 0; i < nk && ok; ++i) {
             ok = mbar_wait(&full[s], ph, p.err, kErrWaitFull, abort_flag);
             ok = __all_sync(0xffffffffu, ok);

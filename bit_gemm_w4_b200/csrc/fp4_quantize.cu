@@ -30,13 +30,29 @@ struct QuantArgs {
     RowSource from;
 };
 
+// A launch that may start while the one before it ends; its kernel waits for
+// that one itself (pdl_wait).
+template <class A>
+cudaError_t launch_after(void (*kernel)(A), const A &args, dim3 grid, dim3 block, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 // ---------------------------------------------------------------- quantise
 // blockDim = (bx, by): bx threads share a row, by rows side by side. A thread
 // holds kChunks chunks of its row, all on their way from memory at once;
 // wider rows are read twice by MQ_FP4_NV, whose row factor needs the whole row
 // first.
 template <class T, bool NV, int kChunks>
-__global__ void __launch_bounds__(512) fp4_quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
     // The launch after this one may start once the launches before are over.
     pdl_wait();
     pdl_launch_dependents();
@@ -124,16 +140,8 @@ mq_status run_quantize(const QuantArgs &a, int bx, cudaStream_t stream) {
     const int by = std::max(1, 128 / bx);
     const long long grid = (a.rows + by - 1) / by;
     if (grid > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 quantisation: too many rows");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(bx, by);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, NV, kChunks>, a);
+    const cudaError_t e = launch_after(fp4_quantize_kernel<T, NV, kChunks>, a, dim3(static_cast<unsigned>(grid)),
+                                       dim3(bx, by), stream);
     if (e != cudaSuccess)
         return fail(MQ_ERR_CUDA, std::string("fp4 quantisation launch: ") + cudaGetErrorString(e));
     return MQ_OK;
@@ -166,7 +174,8 @@ struct DequantArgs {
 // come out of two words and whose scales are at most two. Four units a thread
 // (a block's width apart) are on their way at once.
 template <class T, bool NV>
-__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const DequantArgs a) {
+__global__ void __launch_bounds__(256) fp4_dequantize_kernel(DequantArgs a) {
+    pdl_wait();
     constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
     constexpr int kShift = NV ? 4 : 5;  // log2 of the columns of a block
     constexpr int kUnits = 4;
@@ -177,7 +186,7 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const DequantArgs a
     const uint32_t *words = reinterpret_cast<const uint32_t *>(a.codes + r * a.cpitch);
     const int nwords = static_cast<int>(a.cpitch / 4), K = static_cast<int>(a.K);
     const uint8_t *sc = a.scales + r * a.spitch;
-    const float factor = NV ? __ldg(a.row_scale + r) : 1.0f;
+    const float factor = NV ? load_f32(a.row_scale + r) : 1.0f;
     const int units = (K + lead + kUnit - 1) / kUnit;
     const int u0 = blockIdx.y * (blockDim.x * kUnits) + threadIdx.x;
     // Two codes' values as fp32 pairs: exact in f16, the products with an e4m3
@@ -201,9 +210,9 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const DequantArgs a
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int u = min(u0 + i * static_cast<int>(blockDim.x), units - 1);
-            const uint32_t w = __ldg(words + u / (8 / kUnit));
+            const uint32_t w = load_word(words + u / (8 / kUnit));
             code[i] = kUnit == 8 ? w : w >> (16 * (u & 1));
-            scale[i] = __ldg(sc + ((u * kUnit) >> kShift));
+            scale[i] = load_byte(sc + ((u * kUnit) >> kShift));
         }
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
@@ -239,11 +248,11 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const DequantArgs a
         const int u = min(u0 + i * static_cast<int>(blockDim.x), units - 1);
         const int c0 = u * kUnit - lead;  // negative in the first unit of a row with a lead
         const int w = c0 >> 3, sh = (c0 & 7) * 4;
-        const uint32_t lo = w >= 0 ? __ldg(words + w) : 0u;
-        const uint32_t hi = sh && w + 1 < nwords ? __ldg(words + w + 1) : 0u;
+        const uint32_t lo = w >= 0 ? load_word(words + w) : 0u;
+        const uint32_t hi = sh && w + 1 < nwords ? load_word(words + w + 1) : 0u;
         code[i] = __funnelshift_r(lo, hi, sh);
-        s0[i] = __ldg(sc + (max(c0, 0) >> kShift));
-        s1[i] = __ldg(sc + ((min(c0 + kUnit, K) - 1) >> kShift));
+        s0[i] = load_byte(sc + (max(c0, 0) >> kShift));
+        s1[i] = load_byte(sc + ((min(c0 + kUnit, K) - 1) >> kShift));
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -287,9 +296,8 @@ mq_status run_dequantize(const DequantArgs &a, cudaStream_t stream) {
     const int by = 256 / bx;
     const long long gx = (a.rows + by - 1) / by, gy = (units + bx * 4 - 1) / (bx * 4);
     if (gx > 0x7FFFFFFFll || gy > 65535) return fail(MQ_ERR_UNSUPPORTED, "fp4 dequantisation: too large");
-    fp4_dequantize_kernel<T, NV><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(bx, by), 0,
-                                   stream>>>(a);
-    const cudaError_t e = cudaPeekAtLastError();
+    const cudaError_t e = launch_after(fp4_dequantize_kernel<T, NV>, a,
+                                       dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(bx, by), stream);
     if (e != cudaSuccess)
         return fail(MQ_ERR_CUDA, std::string("fp4 dequantisation launch: ") + cudaGetErrorString(e));
     return MQ_OK;

@@ -6,9 +6,15 @@
 // weight and half of the tokens, so that a byte in shared memory feeds twice
 // the products of a single CTA's tile. At the 4-bit rate a lone CTA would
 // have to write and read 192 bytes of shared memory a cycle, a pair 128.
-// Persistent: one pair for every two SMs walks over the tiles; two
-// accumulators of 224 columns let a tile's outputs be stored while the next
-// tile is computed (2 x 256 would leave no columns for the scales).
+// Persistent: one pair for every two SMs walks over the tiles.
+//
+// Two shapes of tile. Up to 224 tokens (kHalves 1): two accumulators let a
+// tile's outputs be stored while the next tile is computed (2 x 256 columns
+// would leave none for the scales). Up to 384 tokens (kHalves 2): both
+// accumulators belong to one tile, whose weight piece is multiplied with two
+// halves of up to 192 tokens; what has to come from L2 for a product falls by
+// 30 %, and the epilogue packs its outputs into registers first, so that the
+// next tile waits for that alone and not for the stores.
 //
 // Each CTA fills its own ring: warp 0 copies codes and weight scales (TMA),
 // warps 2 to 5 place all the tile's token scales (row-major in memory) in the
@@ -31,11 +37,10 @@ constexpr int kThreads = 448;
 constexpr int kStorers = 8;    // epilogue warps, two for each quarter of the lanes
 constexpr int kMaxStages = 8;
 constexpr int kBoxRows = 16;   // tokens of one copy in a tile that is not full
-constexpr int kMaxTT = 224;    // most tokens of a tile
-constexpr int kLoaders = 4, kLoadRows = (kMaxTT + 32 * kLoaders - 1) / (32 * kLoaders);
+constexpr int kLoaders = 4;
 
 struct WideParams {
-    CUtensorMap tw, tx, tx_small;  // boxes of a piece of the weight, TT / 2 tokens, 16 tokens
+    CUtensorMap tw, tx, tx_small;  // boxes of a piece of the weight, half a MMA's tokens, 16 tokens
     const float *wfactor;
     const uint8_t *xscales;
     const float *xfactor;
@@ -45,35 +50,43 @@ struct WideParams {
     int *err;
     long long N;
     int NT;   // pairs of 128-row tiles
-    int NT1;  // 128-row tiles (of the weight scales)
+    int NT1;  // 128-row tiles
     int KS, E, R;
-    int TT;
+    int TT;   // tokens of a tile, kHalves times a multiple of 32
     int stages;
     int fp16;
     int paired;  // N, the stride and Y's address are even: 4-byte stores
 };
 
-template <bool NV>
+template <bool NV, int kHalves>
 struct WideSmem {
     static constexpr int kUnits = NV ? 4 : 2;
-    static constexpr int kTT = NV ? 192 : kMaxTT;  // columns of one accumulator
-    static constexpr uint32_t kScaleCols = 2 * kTT, kScaleSet = 12 * kUnits;
+    static constexpr int kCols = kHalves == 1 && !NV ? 224 : 192;  // columns of an accumulator
+    // scales in tensor memory: the weight's, then each half's, in one or two sets
+    static constexpr uint32_t kScaleCols = 2 * kCols, kScaleSet = (4 + 8 * kHalves) * kUnits;
+    static constexpr int kSets = kScaleCols + 2 * kScaleSet <= 512 ? 2 : 1;
+    static_assert(kScaleCols + kSets * kScaleSet <= 512, "tensor memory");
     static constexpr int kPiece = kFp4CodePiece + kUnits * 512;
-    __host__ __device__ static int unit(int TT) { return TT > 128 ? 1024 : 512; }  // bytes of a unit of token scales
-    __host__ __device__ static int slot(int TT) { return kPiece + TT * 64 + kUnits * unit(TT); }
-    __host__ __device__ static int total(int TT, int stages) { return slot(TT) * stages + 1024 + 256 + kStorers * kMaxTT * 4; }
+    static constexpr int kFactors = NV ? kStorers * kCols * 4 : 0;
+    // bytes of a unit of one half's scales
+    __host__ __device__ static int unit(int TT) { return TT / kHalves > 128 ? 1024 : 512; }
+    __host__ __device__ static int slot(int TT) { return kPiece + TT * 64 + kHalves * kUnits * unit(TT); }
+    __host__ __device__ static int total(int TT, int stages) { return slot(TT) * stages + 1024 + 256 + kFactors; }
 };
 
-template <bool NV>
+template <bool NV, int kHalves>
 __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_constant__ WideParams p) {
-    using S = WideSmem<NV>;
-    constexpr int kUnits = S::kUnits;
+    using S = WideSmem<NV, kHalves>;
+    constexpr int kUnits = S::kUnits, kBuffers = 3 - kHalves;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int TT = p.TT, stages = p.stages, slot = S::slot(TT), KS = p.KS;
-    const int at_b = S::kPiece, at_sb = at_b + TT * 64, unit = S::unit(TT);
+    const int at_b = S::kPiece, at_sb = at_b + TT * 64, unit = S::unit(TT), HT = TT / kHalves;
+    // tokens of half h of a tile, and the MMA's columns for them
+    auto tokens_of = [&](const Tile &t, int h) { return min(max(t.tokens - h * HT, 0), HT); };
+    auto cols_of = [&](const Tile &t, int h) { return (tokens_of(t, h) + 31) / 32 * 32; };
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + slot * stages);
     uint64_t *full = bars, *empty = bars + kMaxStages, *acc_full = bars + 2 * kMaxStages, *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
@@ -107,27 +120,30 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
         int s = 0, ph = 1, first = 1;
         bool ok = true;
         for (long long ti = pair; ok && walk.find(ti, t); ti += pairs) {
-            const int n = (t.tokens + 31) / 32 * 32;  // the MMA's columns, unless the tile is full
-            const bool whole = n >= TT;
-            const int half = whole ? TT / 2 : n / 2;
-            const uint32_t bytes = 2 * (S::kPiece + half * 128);  // both CTAs' copies
+            int columns = 0;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) columns += cols_of(t, h);
+            const uint32_t bytes = 2 * S::kPiece + columns * 128;  // both CTAs' copies
             // past the last row tile (an odd count) that tile again: rows that are not stored
             const int nt1 = min(t.nt * 2 + static_cast<int>(rank), p.NT1 - 1);
             const int piece = (t.e * p.NT1 + nt1) * KS;
-            const int mb = t.m0 + rank * half;
             auto weight = [&](int k, int slot_i) {
                 const uint32_t bar = in_cta(&full[slot_i], 0);
                 if (rank == 0) mbar_arrive_expect_tx(&full[slot_i], bytes);
                 tma_pair_load_2d(smem + slot_i * slot, &p.tw, bar, 0, (piece + k) * (S::kPiece / 128));
             };
             auto tokens_in = [&](int k, int slot_i) {
-                uint8_t *at = smem + slot_i * slot + at_b;
                 const uint32_t bar = in_cta(&full[slot_i], 0);
-                if (whole)
-                    tma_pair_load_2d(at, &p.tx, bar, k * 128, mb);
-                else
-                    for (int b = 0; b < half; b += kBoxRows)
-                        tma_pair_load_2d(at + b * 128, &p.tx_small, bar, k * 128, mb + b);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    uint8_t *at = smem + slot_i * slot + at_b + h * HT * 64;
+                    const int half = cols_of(t, h) / 2, m = t.m0 + h * HT + rank * half;
+                    if (half == HT / 2)
+                        tma_pair_load_2d(at, &p.tx, bar, k * 128, m);
+                    else
+                        for (int b = 0; b < half; b += kBoxRows)
+                            tma_pair_load_2d(at + b * 128, &p.tx_small, bar, k * 128, m + b);
+                }
             };
             int k = 0;
             if (first) {
@@ -162,10 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
     } else if (warp == 1) {
         int s = 0, ph = 0, b = 0, bph = 1, set = 0;
         bool ok = true;
+        pdl_wait();  // before any wait with a limit: the launch before may take its time
         for (long long ti = pair; ok && walk.find(ti, t); ti += pairs) {
-            const int n = min(TT, (t.tokens + 31) / 32 * 32);
-            const uint32_t desc = tc5::idesc(256, n, !NV);
-            const uint32_t d = tmem + b * S::kTT;
             ok = mbar_wait(&acc_empty[b], bph, p.err, kErrWaitEmpty, abort_flag);
             for (int k = 0; k < KS && ok; ++k) {
                 ok = mbar_wait(&full[s], ph, p.err, kErrWaitFull, abort_flag);
@@ -173,39 +187,48 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                 if (!ok) break;
                 tc5::fence_after();
                 const uint32_t at = smem_u32(smem) + s * slot;
-                const uint32_t sa = at + kFp4CodePiece, sb = at + at_sb;
-                const uint32_t sfa = tmem + S::kScaleCols + set * S::kScaleSet, sfb = sfa + 4 * kUnits;
-                const uint64_t da = tc5::operand_desc(at), db = tc5::operand_desc(at + at_b);
+                const uint32_t sfa = tmem + S::kScaleCols + set * S::kScaleSet;
+                const uint64_t da = tc5::operand_desc(at);
                 if (tc5::elect()) {
 #pragma unroll
-                    for (int u = 0; u < kUnits; ++u) {
-                        tc5::copy_scales<2>(sfa + 4 * u, tc5::scale_desc(sa + 512 * u));
-                        tc5::copy_scales<2>(sfb + 8 * u, tc5::scale_desc(sb + unit * u));
-                        if (n > 128) tc5::copy_scales<2>(sfb + 8 * u + 4, tc5::scale_desc(sb + unit * u + 512));
-                    }
+                    for (int u = 0; u < kUnits; ++u)
+                        tc5::copy_scales<2>(sfa + 4 * u, tc5::scale_desc(at + kFp4CodePiece + 512 * u));
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int u = NV ? q : q >> 1;
-                        const uint32_t byte = NV ? 0 : (q & 1) * 2;
-                        tc5::mma<2, NV>(d, da + 2 * q, db + 2 * q, desc | tc5::idesc_scale_byte(byte), sfa + 4 * u,
-                                        sfb + 8 * u, k > 0 || q > 0);
+                    for (int h = 0; h < kHalves; ++h) {
+                        const int n = cols_of(t, h);
+                        if (n == 0) break;
+                        const uint32_t sfb = sfa + (4 + 8 * h) * kUnits, sb = at + at_sb + h * kUnits * unit;
+                        const uint32_t d = tmem + (kHalves == 2 ? h : b) * S::kCols, desc = tc5::idesc(256, n, !NV);
+                        const uint64_t db = tc5::operand_desc(at + at_b + h * HT * 64);
+#pragma unroll
+                        for (int u = 0; u < kUnits; ++u) {
+                            tc5::copy_scales<2>(sfb + 8 * u, tc5::scale_desc(sb + unit * u));
+                            if (n > 128) tc5::copy_scales<2>(sfb + 8 * u + 4, tc5::scale_desc(sb + unit * u + 512));
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int u = NV ? q : q >> 1;
+                            const uint32_t byte = NV ? 0 : (q & 1) * 2;
+                            tc5::mma<2, NV>(d, da + 2 * q, db + 2 * q, desc | tc5::idesc_scale_byte(byte), sfa + 4 * u,
+                                            sfb + 8 * u, k > 0 || q > 0);
+                        }
                     }
                     tc5::commit_pair(&empty[s]);
                 }
                 __syncwarp();
-                set ^= 1;
+                if (S::kSets == 2) set ^= 1;
                 if (++s == stages) s = 0, ph ^= 1;
             }
             if (tc5::elect()) tc5::commit_pair(&acc_full[b]);
             __syncwarp();
             ok = __all_sync(0xffffffffu, ok);
-            if (++b == 2) b = 0, bph ^= 1;
+            if (++b == kBuffers) b = 0, bph ^= 1;
         }
     } else if (warp < 6) {
         // the tokens' scales, two stages at a time: a row's 32 (MQ_FP4_MX: 16)
         // bytes are read in one go, one pair of stages ahead of their turn
         pdl_wait();
-        constexpr int kVec = NV ? 2 : 1;
+        constexpr int kVec = NV ? 2 : 1, kLoadRows = (kHalves * S::kCols + 32 * kLoaders - 1) / (32 * kLoaders);
         uint4 next[kLoadRows][kVec];
         const int t0 = threadIdx.x - 64;
         auto read = [&](const Tile &tile, int k) {
@@ -252,7 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                     for (int i = 0; i < kLoadRows; ++i) {
                         const int r = t0 + i * 32 * kLoaders;
                         if (r < cur.tokens) {
-                            uint32_t *dst = reinterpret_cast<uint32_t *>(at + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4);
+                            const int h = kHalves == 2 && r >= HT, x = r - h * HT;
+                            uint32_t *dst = reinterpret_cast<uint32_t *>(at + h * kUnits * unit + (x >> 7) * 512 +
+                                                                         (x & 31) * 16 + ((x >> 5) & 3) * 4);
                             const uint4 v = now[i][NV ? j : 0];
                             const int next_unit = unit / 4;
                             if constexpr (NV) {
@@ -277,30 +302,23 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
         // ------------------------------------------------------------ epilogue
         pdl_wait();
         const int quad = warp & 3, row = quad * 32 + lane, which = (warp - 6) >> 2;
-        float *factors = reinterpret_cast<float *>(smem + slot * stages + 256) + (warp - 6) * kMaxTT;
+        float *factors = reinterpret_cast<float *>(smem + slot * stages + 256) + (warp - 6) * S::kCols;
         int b = 0, bph = 0;
         for (long long ti = pair; walk.find(ti, t); ti += pairs) {
             const long long n = (t.nt * 2 + static_cast<int>(rank)) * 128ll + row;
             const bool live = n < p.N;
             const float fw = NV && live ? __ldg(p.wfactor + static_cast<long long>(t.e) * p.N + n) : 1.0f;
+            // the two warps of a quarter take every other 16 tokens of a tile, or a half each
+            const int tokens = kHalves == 2 ? tokens_of(t, which) : t.tokens;
+            const int m0 = t.m0 + (kHalves == 2 ? which * HT : 0);
             if constexpr (NV) {
                 __syncwarp();
-                for (int m = lane; m < t.tokens; m += 32) factors[m] = load_f32(p.xfactor + t.m0 + m);
+                for (int m = lane; m < tokens; m += 32) factors[m] = load_f32(p.xfactor + m0 + m);
                 __syncwarp();
             }
-            if (!mbar_wait_warp(&acc_full[b], bph, p.err, kErrWaitMma, abort_flag)) break;
-            tc5::fence_after();
-            const uint32_t d = tmem + b * S::kTT + (static_cast<uint32_t>(quad) << 21);
-            // every other 16 tokens each, the next ones on their way meanwhile
-            uint32_t next[16];
-            int c = 16 * which;
-            if (c < t.tokens) tc5::load16(d + c, next);
-            for (; c < t.tokens; c += 32) {
-                float v[16];
-                tc5::load_wait();
+            auto outputs = [&](const uint32_t (&bits)[16], int c, float (&v)[16]) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(next[j]);
-                if (c + 32 < t.tokens) tc5::load16(d + c + 32, next);
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(bits[j]);
                 if constexpr (NV) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
@@ -311,13 +329,49 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                         v[j + 3] = v[j + 3] * f.w * fw;
                     }
                 }
-                store_chunk(v, p.Y, p.ldy, t.m0 + c, n, t.tokens - c, live, p.paired, p.fp16);
+            };
+            auto release = [&] {
+                tc5::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(in_cta(&acc_empty[b], 0));
+            };
+            if (!mbar_wait_warp(&acc_full[b], bph, p.err, kErrWaitMma, abort_flag)) break;
+            tc5::fence_after();
+            const uint32_t d = tmem + (kHalves == 2 ? which : b) * S::kCols + (static_cast<uint32_t>(quad) << 21);
+            if constexpr (kHalves == 1) {
+                // the next 16 tokens on their way meanwhile
+                uint32_t next[16];
+                int c = 16 * which;
+                if (c < tokens) tc5::load16(d + c, next);
+                for (; c < tokens; c += 32) {
+                    float v[16];
+                    tc5::load_wait();
+                    outputs(next, c, v);
+                    if (c + 32 < tokens) tc5::load16(d + c + 32, next);
+                    store_chunk(v, p.Y, p.ldy, m0 + c, n, tokens - c, live, p.paired, p.fp16);
+                }
+                release();
+            } else {
+                constexpr int kSteps = S::kCols / 16;
+                uint32_t packed[kSteps][8];
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    if (i * 16 < tokens) {
+                        uint32_t bits[16];
+                        float v[16];
+                        tc5::load16(d + i * 16, bits);
+                        tc5::load_wait();
+                        outputs(bits, i * 16, v);
+                        pack_chunk(v, packed[i], p.paired, p.fp16);
+                    }
+                }
+                release();
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+                    if (i * 16 < tokens)
+                        store_packed(packed[i], p.Y, p.ldy, m0 + i * 16, n, tokens - i * 16, live, p.paired);
             }
-            // the accumulator is read: the next tile but one may use it
-            tc5::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(in_cta(&acc_empty[b], 0));
-            if (++b == 2) b = 0, bph ^= 1;
+            if (++b == kBuffers) b = 0, bph ^= 1;
         }
     }
     __syncwarp();
@@ -335,10 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
 
 }  // namespace
 
-template <bool NV>
+template <bool NV, int kHalves>
 static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,
                           int64_t ldy, bool chained, cudaStream_t stream, int TT) {
-    using S = WideSmem<NV>;
+    using S = WideSmem<NV, kHalves>;
     WideParams p{};
     p.TT = TT;
     p.NT1 = static_cast<int>(d.NT);
@@ -347,7 +401,7 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     const int64_t tiles = (offsets ? std::min<int64_t>(d.E, x.rows) + x.rows / TT : (x.rows + TT - 1) / TT) * p.NT;
     p.stages = std::min(kMaxStages, (227 * 1024 - S::total(TT, 0)) / S::slot(TT));
     p.tw = d.map;
-    if (!encode_bytes_map(&p.tx, x.codes, fp4_code_pitch(d.K), x.rows, TT / 2, true) ||
+    if (!encode_bytes_map(&p.tx, x.codes, fp4_code_pitch(d.K), x.rows, TT / kHalves / 2, true) ||
         !encode_bytes_map(&p.tx_small, x.codes, fp4_code_pitch(d.K), x.rows, kBoxRows, true))
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activations");
     p.paired = d.N % 2 == 0 && ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(Y) & 3) == 0;
@@ -369,7 +423,7 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
     static bool configured[64] = {};
     if (!configured[dev]) {
-        if (cudaFuncSetAttribute(fp4_wide_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+        if (cudaFuncSetAttribute(fp4_wide_kernel<NV, kHalves>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
             cudaSuccess)
             return fail(MQ_ERR_CUDA, "fp4 linear: device setup failed");
         configured[dev] = true;
@@ -388,7 +442,7 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = chained ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_wide_kernel<NV>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_wide_kernel<NV, kHalves>, p);
     if (e != cudaSuccess) return fail(MQ_ERR_CUDA, std::string("fp4 linear launch: ") + cudaGetErrorString(e));
     return MQ_OK;
 }
@@ -397,24 +451,31 @@ mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
                           int64_t ldy, bool chained, cudaStream_t stream) {
     // Tokens of a tile: the choice that leaves the least time over the waves of
     // tiles. A stage takes a time that does not depend on the tokens plus one
-    // for each of them, measured as 0.26 us + 0.46 ns a token (MQ_FP4_MX) and
-    // 0.31 us + 0.8 ns a token (MQ_FP4_NV, whose stages have twice the scales):
-    // 565 and 390 tokens' worth. Matrices of a ragged batch end half a tile
-    // early on average.
+    // for each of them; the constants (ns) fit 8192^3, 4096 x 4096 x 11008 and
+    // 2048 x 14336 x 4096 at 128 to 384 tokens, all of which run at the power
+    // limit. Two halves move less and pay 1 us a tile, for which K has to be
+    // long: 4096 x 4096 x 11008 mxfp4 takes 76 us with 320 tokens and 82 us
+    // with 192, 2048 x 14336 x 4096 nvfp4 84 us with 384 and 73 us with 192.
+    // Matrices of a ragged batch end half a tile early on average.
     const bool nv = d.fmt == MQ_FP4_NV;
     const int64_t NT = (d.NT + 1) / 2, pairs = sm_count() / 2, mats = std::min<int64_t>(d.E, x.rows);
     int best = 0;
     double least = 0;
-    for (int TT = nv ? WideSmem<true>::kTT : WideSmem<false>::kTT; TT >= 32; TT -= 32) {
+    for (int TT : {384, 320, 256, 224, 192, 160, 128, 96, 64, 32}) {
+        if (nv && TT == 224) continue;  // more than its accumulators
+        const bool two = TT > 224;
         const double even = static_cast<double>((x.rows + mats * TT - 1) / (mats * TT)) * mats;
         const double tiles = (mats == 1 ? even : std::max<double>(mats, static_cast<double>(x.rows) / TT + 0.5 * mats)) * NT;
         double waves = tiles / pairs;
         if (mats == 1 || waves < 1) waves = std::ceil(waves);
-        const double cost = waves * (TT + (nv ? 390 : 565));
+        const double stage = nv ? (two ? 200 + 1.67 * TT : 210 + 1.35 * TT) : (two ? 260 + 0.96 * TT : 245 + 0.66 * TT);
+        const double cost = waves * (d.KS * stage + (two ? 1000 : 0));
         if (!best || cost < least) least = cost, best = TT;
     }
-    return d.fmt == MQ_FP4_NV ? run_wide<true>(d, x, offsets, Y, dtype, ldy, chained, stream, best)
-                              : run_wide<false>(d, x, offsets, Y, dtype, ldy, chained, stream, best);
+    if (best > 224) return nv ? run_wide<true, 2>(d, x, offsets, Y, dtype, ldy, chained, stream, best)
+                              : run_wide<false, 2>(d, x, offsets, Y, dtype, ldy, chained, stream, best);
+    return nv ? run_wide<true, 1>(d, x, offsets, Y, dtype, ldy, chained, stream, best)
+              : run_wide<false, 1>(d, x, offsets, Y, dtype, ldy, chained, stream, best);
 }
 
 }  // namespace mq

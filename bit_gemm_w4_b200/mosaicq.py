@@ -484,6 +484,12 @@ def _fmt(fmt) -> int:
     return f
 
 
+def _row_bytes(K: int, fmt: str):
+    """mq_fp4_code_bytes and mq_fp4_scale_bytes."""
+    cols = 256 if fmt == "nvfp4" else 512
+    return (K + 31) // 32 * 16, (K + cols - 1) // cols * 16
+
+
 def _cuda_index(t) -> int:
     index = t.get_device()
     if index < 0:
@@ -548,7 +554,7 @@ class Fp4Tensor:
     """A matrix of microscaled 4-bit values: uint8 codes and scales, a row
     each (layout in mosaicq.h), and for nvfp4 the rows' fp32 factors."""
 
-    __slots__ = ("codes", "scales", "row_scale", "K", "fmt")
+    __slots__ = ("K", "fmt", "rows", "_buffer", "_at", "_codes", "_scales", "_row_scale", "_index")
 
     def __init__(self, codes, scales, row_scale, K: int, fmt: str):
         f = _fmt(fmt)
@@ -566,40 +572,69 @@ class Fp4Tensor:
         if row_scale is not None and (row_scale.dtype != _t.fp32 or row_scale.shape != codes.shape[:-1] or
                                       not row_scale.is_contiguous() or row_scale.device != codes.device):
             raise ValueError("row_scale must be a contiguous float32 tensor, one value for each row")
-        self.codes, self.scales, self.row_scale, self.K, self.fmt = codes, scales, row_scale, K, fmt
-
-    @property
-    def rows(self) -> int:
-        return self.codes.numel() // self.codes.shape[-1]
+        self.K, self.fmt, self.rows = K, fmt, codes.numel() // codes.shape[-1]
+        self._codes, self._scales, self._row_scale = codes, scales, row_scale
+        self._buffer, self._index = None, codes.get_device()
+        self._at = codes.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr()
 
     @classmethod
     def empty(cls, rows: int, K: int, fmt: str, device) -> "Fp4Tensor":
-        """Room for a quantised [rows, K] matrix."""
-        f = _fmt(fmt)
+        """Room for a quantised [rows, K] matrix: one buffer, of which codes,
+        scales and row_scale are views."""
         q = cls.__new__(cls)
-        empty, u8 = _t.empty, _t.u8
-        q.codes = empty((rows, _lib.mq_fp4_code_bytes(K)), dtype=u8, device=device)
-        q.scales = empty((rows, _lib.mq_fp4_scale_bytes(f, K)), dtype=u8, device=device)
-        q.row_scale = empty(rows, dtype=_t.fp32, device=device) if f else None
-        q.K, q.fmt = K, fmt
+        codes, scales = _row_bytes(K, fmt)
+        cut = rows * codes, rows * (codes + scales)
+        q._buffer = b = _t.empty(cut[1] + (4 * rows if fmt == "nvfp4" else 0), dtype=_t.u8, device=device)
+        at = b.data_ptr()
+        q._at = at, at + cut[0], at + cut[1] if fmt == "nvfp4" else None
+        q._codes = q._scales = q._row_scale = None
+        q.K, q.fmt, q.rows, q._index = K, fmt, rows, b.get_device()
         return q
 
-    def _ptrs(self):
-        r = self.row_scale
-        return self.codes.data_ptr(), self.scales.data_ptr(), None if r is None else r.data_ptr()
+    def _view(self, which: int):
+        codes, scales = _row_bytes(self.K, self.fmt)
+        n = self.rows
+        if which == 0:
+            return self._buffer[:n * codes].view(n, codes)
+        if which == 1:
+            return self._buffer[n * codes:n * (codes + scales)].view(n, scales)
+        return self._buffer[n * (codes + scales):].view(_t.fp32)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._view(0)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._view(1)
+        return self._scales
+
+    @property
+    def row_scale(self):
+        if self._row_scale is None and self.fmt == "nvfp4":
+            self._row_scale = self._view(2)
+        return self._row_scale
+
+    @property
+    def device(self):
+        return (self._buffer if self._codes is None else self._codes).device
 
     def dequantize(self, dtype=None, *, stream=None):
         """The values as a [rows, K] tensor (fp32 unless a dtype is given)."""
-        index = _cuda_index(self.codes)
+        index = self._index
+        if index < 0:
+            raise ValueError(f"a CUDA tensor is needed, not one on {self.device}")
         if _elsewhere(index, stream):
             with _On(index, stream):
                 return self.dequantize(dtype)
         dtype = _t.fp32 if dtype is None else dtype
         d = _dtype(dtype, "dequantize", fp32=True)
         rows, K = self.rows, self.K
-        Y = _t.empty((rows, K), dtype=dtype, device=self.codes.device)
-        st = _lib.mq_fp4_dequantize(*self._ptrs(), rows, K, FP4_FORMATS[self.fmt], Y.data_ptr(), d, K,
-                                    _t.raw_stream(index))
+        Y = _t.empty((rows, K), dtype=dtype, device=self.device)
+        st = _lib.mq_fp4_dequantize(*self._at, rows, K, FP4_FORMATS[self.fmt], Y.data_ptr(), d, K, _t.raw_stream(index))
         if st:
             _check(st, "mq_fp4_dequantize")
         return Y
@@ -621,7 +656,7 @@ def fp4_quantize(X, fmt: str = "nvfp4", *, rows=None, stream=None) -> Fp4Tensor:
         rows = _index(rows, index, "rows")
         R, at = rows.shape[0], rows.data_ptr()
     q = Fp4Tensor.empty(R, K, fmt, X.device)
-    st = _lib.mq_fp4_quantize(X.data_ptr(), d, R, K, ldx, at, M, f, *q._ptrs(), _t.raw_stream(index))
+    st = _lib.mq_fp4_quantize(X.data_ptr(), d, R, K, ldx, at, M, f, *q._at, _t.raw_stream(index))
     if st:
         _check(st, "mq_fp4_quantize")
     return q
@@ -638,6 +673,7 @@ class Fp4Weight:
         self.E, self.N, self.K, self.device_bytes = i.E, i.N, i.K, i.device_bytes
         self.fmt = {v: k for k, v in FP4_FORMATS.items()}[i.format]
         self._index = i.device
+        self._workspace_bytes = {}  # rows -> bytes
         self.device = _t.torch.device("cuda", i.device)
 
     @classmethod
@@ -672,7 +708,7 @@ class Fp4Weight:
                 return cls.pack_codes(codes, scales, row_scale, K, fmt)
         h = ctypes.c_void_p()
         E = codes.shape[0] if codes.dim() == 3 else 1
-        _check(_lib.mq_fp4_pack_codes(*q._ptrs(), E, codes.shape[-2], q.K, FP4_FORMATS[fmt], _t.raw_stream(index),
+        _check(_lib.mq_fp4_pack_codes(*q._at, E, codes.shape[-2], q.K, FP4_FORMATS[fmt], _t.raw_stream(index),
                                       ctypes.byref(h)), "mq_fp4_pack_codes")
         return cls(h.value)
 
@@ -689,12 +725,13 @@ class Fp4Weight:
             with _On(self._index, stream):
                 return self.export()
         q = Fp4Tensor.empty(self.E * self.N, self.K, self.fmt, self.device)
-        _check(_lib.mq_fp4_export(self._h, *q._ptrs(), _t.raw_stream(self._index)), "mq_fp4_export")
+        _check(_lib.mq_fp4_export(self._h, *q._at, _t.raw_stream(self._index)), "mq_fp4_export")
         return q
 
     def _output(self, Y, rows: int, dtype):
         if Y is None:
-            return _t.empty((rows, self.N), dtype=dtype, device=self.device), self.N
+            N = self.N
+            return _t.empty((rows, N), dtype=dtype, device=self.device), N
         if Y.device != self.device or Y.dtype != dtype or Y.shape != (rows, self.N) or \
                 (Y.stride(1) != 1 and self.N > 1) or (Y.stride(0) < self.N and rows > 1):
             raise ValueError(f"Y must be a {dtype} [{rows}, {self.N}] tensor on {self.device} with contiguous rows")
@@ -702,7 +739,11 @@ class Fp4Weight:
 
     def _workspace(self, workspace, rows: int):
         if workspace is None:
-            n = _lib.mq_fp4_workspace_bytes(self._h, rows)
+            n = self._workspace_bytes.get(rows)
+            if n is None:
+                n = self._workspace_bytes[rows] = self.workspace_bytes(rows)
+                if len(self._workspace_bytes) > 4096:
+                    self._workspace_bytes = {}
             if not n:
                 return None, None, 0
             workspace = _t.empty(n, dtype=_t.u8, device=self.device)
@@ -712,7 +753,7 @@ class Fp4Weight:
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
     def _quantized(self, X: Fp4Tensor, dtype):
-        if X.fmt != self.fmt or X.K != self.K or X.codes.get_device() != self._index:
+        if X.fmt != self.fmt or X.K != self.K or X._index != self._index:
             raise ValueError(f"the activations must be {self.fmt} with K = {self.K} on {self.device}")
         dtype = _t.bf16 if dtype is None else dtype
         return dtype, _dtype(dtype, "the output")
@@ -736,7 +777,7 @@ class Fp4Weight:
         if isinstance(X, Fp4Tensor):
             dtype, d = self._quantized(X, dtype)
             Y, ldy = self._output(Y, X.rows, dtype)
-            st = _lib.mq_fp4_linear_codes(self._h, *X._ptrs(), X.rows, Y.data_ptr(), d, ldy, _t.raw_stream(index))
+            st = _lib.mq_fp4_linear_codes(self._h, *X._at, X.rows, Y.data_ptr(), d, ldy, _t.raw_stream(index))
             if st:
                 _check(st, "mq_fp4_linear_codes")
             return Y
@@ -767,7 +808,7 @@ class Fp4Weight:
                 raise ValueError("rows are taken when X is quantised: fp4_quantize(X, rows=rows)")
             dtype, d = self._quantized(X, dtype)
             Y, ldy = self._output(Y, X.rows, dtype)
-            st = _lib.mq_fp4_linear_grouped_codes(self._h, *X._ptrs(), X.rows, offsets.data_ptr(), Y.data_ptr(), d,
+            st = _lib.mq_fp4_linear_grouped_codes(self._h, *X._at, X.rows, offsets.data_ptr(), Y.data_ptr(), d,
                                                   ldy, _t.raw_stream(index))
             if st:
                 _check(st, "mq_fp4_linear_grouped_codes")
