@@ -61,10 +61,12 @@ constexpr int fp4_piece(int fmt) { return kFp4CodePiece + fp4_scale_piece(fmt); 
 
 // X (dtype, row stride ldx elements) to codes, scales and (MQ_FP4_NV) row
 // factors, `rows` output rows; output row r is X row index[r] (index NULL: r),
-// and a row of zeros where index[r] is outside [0, x_rows).
+// and a row of zeros where index[r] is outside [0, x_rows). `open`: the launch
+// that follows may start at once (it waits for this one before it reads
+// anything but packed weights).
 mq_status launch_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64_t K, int64_t ldx,
                               const int32_t *index, int64_t x_rows, int fmt, uint8_t *codes,
-                              uint8_t *scales, float *row_scale, cudaStream_t stream);
+                              uint8_t *scales, float *row_scale, bool open, cudaStream_t stream);
 
 mq_status launch_fp4_dequantize(const Fp4Rows &x, int64_t K, int fmt, void *Y, mq_dtype dtype,
                                 int64_t ldy, cudaStream_t stream);
@@ -74,8 +76,8 @@ mq_status launch_fp4_order(const Fp4Device &d, uint8_t *codes, uint8_t *scales, 
 
 // Y[r] = x[r] * W[e]^T for the rows offsets[e] <= r < offsets[e + 1] of every
 // e (offsets NULL: E is 1 and every row belongs to it). `chained`: x was
-// written by the launch just before on this stream, which lets this one start
-// early.
+// written by the launch just before on this stream, which started after the
+// offsets were there.
 mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                             mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
 

@@ -160,7 +160,7 @@ mq_status quantize_and_multiply(const mq_fp4_weight *w, const void *X, int dtype
     uint8_t *base = static_cast<uint8_t *>(workspace);
     float *factors = d.fmt == MQ_FP4_NV ? reinterpret_cast<float *>(base + ws.factors) : nullptr;
     if (mq_status st = launch_fp4_quantize(X, static_cast<mq_dtype>(dtype), R, d.K, ldx, index, x_rows, d.fmt, base,
-                                           base + ws.scales, factors, s))
+                                           base + ws.scales, factors, offsets == nullptr, s))
         return st;
     const Fp4Rows x{base, base + ws.scales, factors, R};
     return launch_fp4_linear(d, x, offsets, Y, static_cast<mq_dtype>(dtype), ldy, true, s);
@@ -208,7 +208,7 @@ mq_status mq_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64_t K
     if (rows == 0) return MQ_OK;
     if (mq_status st = check_quantized(codes, scales, row_scale, fmt)) return st;
     return launch_fp4_quantize(X, dtype, rows, K, ldx, index, x_rows, fmt, static_cast<uint8_t *>(codes),
-                               static_cast<uint8_t *>(scales), row_scale, reinterpret_cast<cudaStream_t>(stream));
+                               static_cast<uint8_t *>(scales), row_scale, true, reinterpret_cast<cudaStream_t>(stream));
 }
 
 mq_status mq_fp4_dequantize(const void *codes, const void *scales, const float *row_scale, int64_t rows, int64_t K,
@@ -292,7 +292,8 @@ mq_status mq_fp4_pack(const void *W, mq_dtype dtype, int64_t E, int64_t N, int64
         if (e != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack");
     }
     if (!st)
-        st = launch_fp4_quantize(W, dtype, E * N, K, K, nullptr, E * N, fmt, rows, rows + code_bytes, w->d.row_scale, s);
+        st = launch_fp4_quantize(W, dtype, E * N, K, K, nullptr, E * N, fmt, rows, rows + code_bytes, w->d.row_scale,
+                                 false, s);
     if (!st) st = launch_fp4_order(w->d, rows, rows + code_bytes, false, s);
     if (rows) {
         e = cudaStreamSynchronize(s);

@@ -58,6 +58,7 @@ struct NarrowParams {
     int stages;  // ring slots
     int fp16;    // Y's type
     int paired;  // N, the stride and Y's address are even: 4-byte stores
+    int wait_first;
 };
 
 // Shared memory: the ring (a piece of the weight, the tokens' codes and scales
@@ -118,9 +119,10 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
     if constexpr (kQuantise)
         if (threadIdx.x >= 64)
             for (int i = threadIdx.x - 64; i < TT; i += kFeeders) tops[i] = 0;
-    // Offsets may come from the launch just before; a chained launch starts
-    // only when the one that quantised its tokens has seen them complete.
-    if (kQuantise && p.offsets) pdl_wait();
+    // Whatever follows on the stream may start: it waits for this launch
+    // before it reads anything but packed weights.
+    pdl_launch_dependents();
+    if (p.wait_first) pdl_wait();  // the offsets may come from the launch just before
     Tile t{0, 0, 0, 0};
     TileWalk walk(p.offsets, p.E, p.R, TT, p.NT);
     const bool live = walk.find(blockIdx.x / split, t);  // the same in every CTA of a cluster
@@ -460,6 +462,7 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
     p.KS = d.KS;
     p.E = static_cast<int>(d.E);
     p.R = static_cast<int>(rows);
+    p.wait_first = p.offsets && !chained;
     p.paired = d.N % 2 == 0 && p.ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 3) == 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(MQ_ERR_CUDA, "cudaGetDevice failed");
@@ -485,11 +488,9 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
         attr[na].val.clusterDim.z = 1;
         ++na;
     }
-    if (chained) {
-        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[na].val.programmaticStreamSerializationAllowed = 1;
-        ++na;
-    }
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
     cfg.attrs = attr;
     cfg.numAttrs = na;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_narrow_kernel<NV, T>, p);
@@ -566,10 +567,10 @@ mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype d
     p.ldy = ldy;
     p.fp16 = dtype == MQ_FP16;
     if (dtype == MQ_FP16)
-        return d.fmt == MQ_FP4_NV ? run_narrow<true, __half>(d, p, rows, 16, c.likely, true, stream)
-                                  : run_narrow<false, __half>(d, p, rows, 16, c.likely, true, stream);
-    return d.fmt == MQ_FP4_NV ? run_narrow<true, __nv_bfloat16>(d, p, rows, 16, c.likely, true, stream)
-                              : run_narrow<false, __nv_bfloat16>(d, p, rows, 16, c.likely, true, stream);
+        return d.fmt == MQ_FP4_NV ? run_narrow<true, __half>(d, p, rows, 16, c.likely, false, stream)
+                                  : run_narrow<false, __half>(d, p, rows, 16, c.likely, false, stream);
+    return d.fmt == MQ_FP4_NV ? run_narrow<true, __nv_bfloat16>(d, p, rows, 16, c.likely, false, stream)
+                              : run_narrow<false, __nv_bfloat16>(d, p, rows, 16, c.likely, false, stream);
 }
 
 }  // namespace mq

@@ -28,6 +28,7 @@ struct QuantArgs {
     long long rows;
     long long cpitch, spitch;  // bytes of a row of codes, of scales
     RowSource from;
+    bool open;
 };
 
 // A launch that may start while the one before it ends; its kernel waits for
@@ -53,9 +54,12 @@ cudaError_t launch_after(void (*kernel)(A), const A &args, dim3 grid, dim3 block
 // first.
 template <class T, bool NV, int kChunks>
 __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
-    // The launch after this one may start once the launches before are over.
+    // The launch after this one starts early: at once when all it looks at
+    // before its own wait is a packed weight, else when the launches before
+    // this one are over.
+    if (a.open) pdl_launch_dependents();
     pdl_wait();
-    pdl_launch_dependents();
+    if (!a.open) pdl_launch_dependents();
     __shared__ uint32_t wmax[16];
     const int bx = blockDim.x, tx = threadIdx.x, ty = threadIdx.y;
     const int chunks = static_cast<int>(NV ? a.spitch : a.spitch * 2);  // the scales' padding included
@@ -175,6 +179,7 @@ struct DequantArgs {
 // (a block's width apart) are on their way at once.
 template <class T, bool NV>
 __global__ void __launch_bounds__(256) fp4_dequantize_kernel(DequantArgs a) {
+    pdl_launch_dependents();
     pdl_wait();
     constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
     constexpr int kShift = NV ? 4 : 5;  // log2 of the columns of a block
@@ -344,11 +349,11 @@ __global__ void __launch_bounds__(256) fp4_order_kernel(uint8_t *pieces, uint8_t
 
 mq_status launch_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64_t K, int64_t ldx,
                               const int32_t *index, int64_t x_rows, int fmt, uint8_t *codes,
-                              uint8_t *scales, float *row_scale, cudaStream_t stream) {
+                              uint8_t *scales, float *row_scale, bool open, cudaStream_t stream) {
     if (rows <= 0) return MQ_OK;
     const int64_t size = dtype == MQ_FP32 ? 4 : 2;
     QuantArgs a{X, ldx, x_rows, index, codes, scales, row_scale, rows, fp4_code_pitch(K), fp4_scale_pitch(fmt, K),
-                {K, static_cast<const char *>(X), static_cast<const char *>(X) + ((x_rows - 1) * ldx + K) * size}};
+                {K, static_cast<const char *>(X), static_cast<const char *>(X) + ((x_rows - 1) * ldx + K) * size}, open};
     const bool nv = fmt == MQ_FP4_NV;
     switch (dtype) {
         case MQ_BF16: return nv ? pick_quantize<__nv_bfloat16, true>(a, stream) : pick_quantize<__nv_bfloat16, false>(a, stream);

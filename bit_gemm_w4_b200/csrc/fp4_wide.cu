@@ -56,6 +56,7 @@ struct WideParams {
     int stages;
     int fp16;
     int paired;  // N, the stride and Y's address are even: 4-byte stores
+    int wait_first;
 };
 
 template <bool NV, int kHalves>
@@ -112,6 +113,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
     tc5::fence_after();
     const uint32_t tmem = *tmem_slot;
 
+    // Whatever follows on the stream may start: it waits for this launch
+    // before it reads anything but packed weights.
+    pdl_launch_dependents();
+    if (p.wait_first) pdl_wait();  // the offsets may come from the launch just before
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     TileWalk walk(p.offsets, p.E, p.R, TT, p.NT);
     Tile t;
@@ -418,6 +423,7 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     p.E = static_cast<int>(d.E);
     p.R = static_cast<int>(x.rows);
     p.fp16 = dtype == MQ_FP16;
+    p.wait_first = offsets && !chained;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(MQ_ERR_CUDA, "cudaGetDevice failed");
     if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
@@ -441,7 +447,7 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = chained ? 2 : 1;
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_wide_kernel<NV, kHalves>, p);
     if (e != cudaSuccess) return fail(MQ_ERR_CUDA, std::string("fp4 linear launch: ") + cudaGetErrorString(e));
     return MQ_OK;

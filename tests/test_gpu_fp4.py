@@ -172,7 +172,7 @@ def test_linear(mq, cuda, fmt, dtype, M, N, K):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", [(1, 8192, 11008), (16, 14336, 4096), (96, 4096, 4096), (1000, 4096, 2048),
-                                   (2048, 2560, 4096)])
+                                   (2048, 2560, 4096), (4096, 4096, 11008), (2000, 9001, 11008), (4000, 4096, 11008)])
 def test_linear_large(mq, cuda, fmt, M, N, K):
     # sampled rows of W and of X: the whole range of tiles, the rest by columns
     X, W = values(M, K, BF16, M, spread=0.3), values(N, K, BF16, N, spread=0.3) * 0.05
