@@ -47,6 +47,7 @@ struct Fp4Rows {
 struct Fp4Device {
     int64_t E = 0, N = 0, K = 0;
     int fmt = 0;
+    int device = 0, sms = 0;
     int KS = 0;      // K stages
     int64_t NT = 0;  // 128-row tiles of one matrix
     uint8_t *pieces = nullptr;

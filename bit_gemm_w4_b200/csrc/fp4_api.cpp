@@ -83,6 +83,8 @@ mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
     d.N = N;
     d.K = K;
     d.fmt = fmt;
+    d.device = w->device;
+    d.sms = sm_count();
     d.KS = static_cast<int>((K + kFp4StageK - 1) / kFp4StageK);
     d.NT = (N + 127) / 128;
     auto get = [&](void **p, int64_t bytes) {
@@ -106,6 +108,7 @@ mq_status new_weight(mq_fp4_weight **out) {
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "no usable CUDA device");
+    if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
     mq_fp4_weight *w = new (std::nothrow) mq_fp4_weight();
     if (!w) return fail(MQ_ERR_OUT_OF_MEMORY, "host allocation failed");
     w->device = dev;

@@ -450,7 +450,7 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
     // with 1 and 14.0 us with 4).
     const int each = (113 * 1024 - S::fixed(p.TT, 8)) / S::slot(p.TT) >= 4 ? 2 : 1;
     const int budget = each == 2 ? 113 * 1024 : 227 * 1024;
-    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sm_count() / likely})));
+    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, d.sms / likely})));
     if (tiles * p.split > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 linear: too many tiles");
     p.stages = std::min(kMaxStages, (budget - S::fixed(p.TT, p.split)) / S::slot(p.TT));
     const int smem = S::total(p.TT, p.split, p.stages);
@@ -464,15 +464,12 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
     p.R = static_cast<int>(rows);
     p.wait_first = p.offsets && !chained;
     p.paired = d.N % 2 == 0 && p.ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 3) == 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return fail(MQ_ERR_CUDA, "cudaGetDevice failed");
-    if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
     static bool configured[64] = {};
-    if (!configured[dev]) {
+    if (!configured[d.device]) {
         if (cudaFuncSetAttribute(fp4_narrow_kernel<NV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
             cudaSuccess)
             return fail(MQ_ERR_CUDA, "fp4 linear: device setup failed");
-        configured[dev] = true;
+        configured[d.device] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
@@ -507,7 +504,7 @@ struct Choice {
 
 Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
     const int64_t mats = grouped ? std::min<int64_t>(d.E, rows) : 1, per = (rows + mats - 1) / mats;
-    const int64_t sms = sm_count();
+    const int64_t sms = d.sms;
     // Up to 32 tokens: narrow, as long as its tiles run in one wave of two CTAs
     // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
     // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 64: narrow

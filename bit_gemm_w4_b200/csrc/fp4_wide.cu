@@ -424,18 +424,15 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     p.R = static_cast<int>(x.rows);
     p.fp16 = dtype == MQ_FP16;
     p.wait_first = offsets && !chained;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return fail(MQ_ERR_CUDA, "cudaGetDevice failed");
-    if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
     static bool configured[64] = {};
-    if (!configured[dev]) {
+    if (!configured[d.device]) {
         if (cudaFuncSetAttribute(fp4_wide_kernel<NV, kHalves>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
             cudaSuccess)
             return fail(MQ_ERR_CUDA, "fp4 linear: device setup failed");
-        configured[dev] = true;
+        configured[d.device] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, sm_count() / 2)));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, d.sms / 2)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::total(TT, p.stages);
     cfg.stream = stream;
@@ -464,7 +461,7 @@ mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     // with 192, 2048 x 14336 x 4096 nvfp4 84 us with 384 and 73 us with 192.
     // Matrices of a ragged batch end half a tile early on average.
     const bool nv = d.fmt == MQ_FP4_NV;
-    const int64_t NT = (d.NT + 1) / 2, pairs = sm_count() / 2, mats = std::min<int64_t>(d.E, x.rows);
+    const int64_t NT = (d.NT + 1) / 2, pairs = d.sms / 2, mats = std::min<int64_t>(d.E, x.rows);
     int best = 0;
     double least = 0;
     for (int TT : {384, 320, 256, 224, 192, 160, 128, 96, 64, 32}) {

@@ -461,7 +461,8 @@ class _Lazy:
         self.empty = torch.empty
         self.bf16, self.fp32, self.u8 = torch.bfloat16, torch.float32, torch.uint8
         self.dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # mq_dtype
-        self.current_device = torch.cuda.current_device
+        self.int32 = torch.int32
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
         return self.__dict__[name]
@@ -542,6 +543,8 @@ def _rows_view(X, where: str):
 
 
 def _index(t, index: int, where: str):
+    if t.dtype is _t.int32 and t.get_device() == index and t.dim() == 1 and t.is_contiguous():
+        return t
     torch = _t.torch
     if t.get_device() != index or t.dim() != 1 or t.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"{where} must be a 1-D int32 or int64 tensor on cuda:{index}")
@@ -730,8 +733,7 @@ class Fp4Weight:
 
     def _output(self, Y, rows: int, dtype):
         if Y is None:
-            N = self.N
-            return _t.empty((rows, N), dtype=dtype, device=self.device), N
+            return _t.empty((rows, self.N), dtype=dtype, device=self.device), self.N
         if Y.device != self.device or Y.dtype != dtype or Y.shape != (rows, self.N) or \
                 (Y.stride(1) != 1 and self.N > 1) or (Y.stride(0) < self.N and rows > 1):
             raise ValueError(f"Y must be a {dtype} [{rows}, {self.N}] tensor on {self.device} with contiguous rows")
@@ -759,12 +761,18 @@ class Fp4Weight:
         return dtype, _dtype(dtype, "the output")
 
     def _input(self, X, dtype):
-        d = _dtype(X.dtype, "X")
-        if dtype is not None and dtype != X.dtype:
-            raise ValueError("Y has the type of X; dtype is for quantised activations")
-        if X.get_device() != self._index or X.dim() != 2 or X.shape[1] != self.K:
+        d = _t.dtypes.get(X.dtype, 2)
+        shape = X.shape
+        if d == 2 or (dtype is not None and dtype != X.dtype):
+            raise ValueError("X must be bf16 or fp16, and Y has its type (dtype is for quantised activations)")
+        if len(shape) != 2 or shape[1] != self.K or X.get_device() != self._index:
             raise ValueError(f"X must be a [rows, {self.K}] tensor on {self.device}")
-        return d, *_rows_view(X, "X")
+        M, K = shape
+        ld, one = X.stride()
+        if M > 1 and one == 1 and ld >= K:
+            return d, X, M, ld
+        X, _, _, ld = _rows_view(X, "X")
+        return d, X, M, ld
 
     def linear(self, X, Y=None, workspace=None, *, dtype=None, stream=None):
         """Y = X @ W^T. X: a bf16 or fp16 [M, K] tensor, quantised within the
@@ -781,8 +789,8 @@ class Fp4Weight:
             if st:
                 _check(st, "mq_fp4_linear_codes")
             return Y
-        d, X, M, _, ldx = self._input(X, dtype)
-        Y, ldy = self._output(Y, M, X.dtype)
+        d, X, M, ldx = self._input(X, dtype)
+        Y, ldy = (X.new_empty((M, self.N)), self.N) if Y is None else self._output(Y, M, X.dtype)
         workspace, at_ws, nbytes = self._workspace(workspace, M)
         st = _lib.mq_fp4_linear(self._h, X.data_ptr(), d, M, ldx, Y.data_ptr(), ldy, at_ws, nbytes,
                                 _t.raw_stream(index))
@@ -813,12 +821,12 @@ class Fp4Weight:
             if st:
                 _check(st, "mq_fp4_linear_grouped_codes")
             return Y
-        d, X, M, _, ldx = self._input(X, dtype)
+        d, X, M, ldx = self._input(X, dtype)
         R, at = M, None
         if rows is not None:
             rows = _index(rows, index, "rows")
             R, at = rows.shape[0], rows.data_ptr()
-        Y, ldy = self._output(Y, R, X.dtype)
+        Y, ldy = (X.new_empty((R, self.N)), self.N) if Y is None else self._output(Y, R, X.dtype)
         workspace, at_ws, nbytes = self._workspace(workspace, R)
         st = _lib.mq_fp4_linear_grouped(self._h, X.data_ptr(), d, M, ldx, at, R, offsets.data_ptr(), Y.data_ptr(), ldy,
                                         at_ws, nbytes, _t.raw_stream(index))
