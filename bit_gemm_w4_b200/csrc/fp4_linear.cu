@@ -230,10 +230,13 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
             auto chunk = [&](int r, long long c) {
                 Raw<T> raw;
                 const long long x = sources[r];
-                if (x >= 0 && x < p.x_rows)
-                    load_chunk(raw, p.from, static_cast<const T *>(p.X) + x * p.ldx, c);
-                else
+                const T *row = static_cast<const T *>(p.X) + x * p.ldx;
+                if (x < 0 || x >= p.x_rows)
                     raw.clear();
+                else if ((reinterpret_cast<uintptr_t>(row) & 31) == 0 && c + kChunk <= p.from.K)
+                    load_whole_chunk(raw, row + c);
+                else
+                    load_chunk(raw, p.from, row, c);
                 return raw;
             };
             if constexpr (NV) {
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
                 for (int x = warp - 2; x < tokens * parts; x += kFeeders / 32) {
                     const int r = x / parts;
                     uint32_t m = 0;
-#pragma unroll 4
+#pragma unroll 8
                     for (int c = (x - r * parts) * 32 + lane; c < chunks; c += 32 * parts)
                         m = max(m, chunk(r, static_cast<long long>(c) * kChunk).max_bits());
                     m = __reduce_max_sync(0xffffffffu, m);
@@ -437,20 +440,16 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
 }
 
 template <bool NV, class T>
-mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, int64_t likely, bool chained,
+mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, int split, bool chained,
                      cudaStream_t stream) {
     using S = NarrowSmem<NV>;
     p.TT = TT;
     // the most tiles that any split of the rows into matrices makes
     const int64_t tiles = (p.offsets ? std::min<int64_t>(d.E, rows) + rows / p.TT : (rows + p.TT - 1) / p.TT) * d.NT;
-    // Two CTAs an SM where each then has a ring of four stages, else one. K is
-    // split as far as that gives every SM at most one CTA: past it the further
-    // CTAs start after the first ones' loads (1 x 4096 x 4096 takes 9.1, 8.0,
-    // 8.5 and 9.3 us with 2, 4, 6 and 8; 1 x 11008 x 4096, 86 tiles, 11.8 us
-    // with 1 and 14.0 us with 4).
+    p.split = split;
+    // Two CTAs an SM where each then has a ring of four stages, else one.
     const int each = (113 * 1024 - S::fixed(p.TT, 8)) / S::slot(p.TT) >= 4 ? 2 : 1;
     const int budget = each == 2 ? 113 * 1024 : 227 * 1024;
-    p.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, d.sms / likely})));
     if (tiles * p.split > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 linear: too many tiles");
     p.stages = std::min(kMaxStages, (budget - S::fixed(p.TT, p.split)) / S::slot(p.TT));
     const int smem = S::total(p.TT, p.split, p.stages);
@@ -499,7 +498,9 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
 // known to the host: `per` is their average).
 struct Choice {
     int TT;          // tokens of a narrow tile; 0: the wide form
+    int split;       // CTAs that share a narrow tile
     int64_t likely;  // narrow tiles of the matrices that have rows
+    int64_t per;     // rows of a matrix that has some
 };
 
 Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
@@ -512,8 +513,13 @@ Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
     // 4096 x 11008: 14.4 us, wide 20.1; 64 x 11008 x 4096: 12.1 us, wide 11.6).
     const int TT = per <= 16 ? 16 : per <= 32 ? 32 : 64;
     const int64_t likely = mats * d.NT;
-    if (per <= 32 ? likely <= 2 * sms : per <= 64 && likely <= sms / 2) return {TT, likely};
-    return {0, likely};
+    const bool narrow = per <= 32 ? likely <= 2 * sms : per <= 64 && likely <= sms / 2;
+    // K is split as far as that gives every SM at most one CTA: past it the
+    // further CTAs start after the first ones' loads (1 x 4096 x 4096 takes
+    // 9.1, 8.0, 8.5 and 9.3 us with 2, 4, 6 and 8; 1 x 11008 x 4096, 86 tiles,
+    // 11.8 us with 1 and 14.0 us with 4).
+    const int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sms / likely})));
+    return {narrow ? TT : 0, split, likely, per};
 }
 
 }  // namespace
@@ -533,19 +539,24 @@ mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t 
     p.Y = Y;
     p.ldy = ldy;
     p.fp16 = dtype == MQ_FP16;
-    return d.fmt == MQ_FP4_NV ? run_narrow<true, void>(d, p, x.rows, c.TT, c.likely, chained, stream)
-                              : run_narrow<false, void>(d, p, x.rows, c.TT, c.likely, chained, stream);
+    return d.fmt == MQ_FP4_NV ? run_narrow<true, void>(d, p, x.rows, c.TT, c.split, chained, stream)
+                              : run_narrow<false, void>(d, p, x.rows, c.TT, c.split, chained, stream);
 }
 
-// One or two rows a matrix and little weight to read: the launch saved is
-// worth what every CTA's own quantisation costs (1 x 4096 x 4096: 8.4 us of the
-// device's time against 8.0 us, and one launch of the host's instead of two;
-// at four rows it is 9.4 against 7.9 us).
+// Whether the product quantises its tokens itself: the launch and the round
+// through memory saved against every CTA's own quantisation, which for
+// MQ_FP4_NV includes a look at the whole of each row. It is taken where it
+// costs the device at most 2 us more (nvfp4 4096 x 4096, 1 / 4 / 8 / 16 rows:
+// 6.3 / 7.4 / 9.2 / 13.4 us against 6.7 / 6.8 / 7.2 / 7.6 us; mxfp4 4.7 / 4.9 /
+// 6.0 / 7.6 against 5.8 / 5.8 / 6.1 / 6.4 us): the host's share of a launch is
+// 3 us. A CTA with more stages than its ring (11008 x 4096) quantises while
+// its loads wait, and large weights leave no time to hide it in.
 bool fp4_linear_quantises(const Fp4Device &d, int64_t rows) {
     const Choice c = choose(d, rows, d.E > 1);
-    const int64_t mats = std::min<int64_t>(d.E, rows);
-    return c.TT == 16 && rows <= 2 * mats && c.likely * d.KS * fp4_piece(d.fmt) <= (int64_t(40) << 20) &&
-           (d.fmt == MQ_FP4_MX || d.K <= 16384);
+    if (c.TT != 16 || c.likely * d.KS * fp4_piece(d.fmt) > (int64_t(40) << 20)) return false;
+    const int64_t stages = (d.KS + c.split - 1) / c.split;
+    if (d.fmt == MQ_FP4_MX) return stages <= 5 || c.per <= 8;
+    return c.per * d.K <= (stages <= 5 ? 32768 : 0);
 }
 
 mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype dtype, int64_t rows, int64_t ldx,
@@ -564,10 +575,10 @@ mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype d
     p.ldy = ldy;
     p.fp16 = dtype == MQ_FP16;
     if (dtype == MQ_FP16)
-        return d.fmt == MQ_FP4_NV ? run_narrow<true, __half>(d, p, rows, 16, c.likely, false, stream)
-                                  : run_narrow<false, __half>(d, p, rows, 16, c.likely, false, stream);
-    return d.fmt == MQ_FP4_NV ? run_narrow<true, __nv_bfloat16>(d, p, rows, 16, c.likely, false, stream)
-                              : run_narrow<false, __nv_bfloat16>(d, p, rows, 16, c.likely, false, stream);
+        return d.fmt == MQ_FP4_NV ? run_narrow<true, __half>(d, p, rows, 16, c.split, false, stream)
+                                  : run_narrow<false, __half>(d, p, rows, 16, c.split, false, stream);
+    return d.fmt == MQ_FP4_NV ? run_narrow<true, __nv_bfloat16>(d, p, rows, 16, c.split, false, stream)
+                              : run_narrow<false, __nv_bfloat16>(d, p, rows, 16, c.split, false, stream);
 }
 
 }  // namespace mq

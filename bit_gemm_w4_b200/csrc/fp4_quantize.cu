@@ -157,11 +157,13 @@ mq_status pick_quantize(const QuantArgs &a, cudaStream_t stream) {
     auto threads = [&](int per) {
         return static_cast<int>(std::min<long long>(512, ((chunks + per - 1) / per + 31) / 32 * 32));
     };
-    // Few rows: spread over threads, for the shortest way from load to store.
-    // Many: as many chunks a thread as a row has for a warp, up to four.
-    if (chunks <= 32 || (a.rows * chunks <= 512ll * sm_count() && chunks <= 512))
-        return run_quantize<T, NV, 1>(a, threads(1), stream);
-    if (chunks <= 64) return run_quantize<T, NV, 2>(a, 32, stream);
+    // Chunks a thread: one while all of them find a thread at once, two up to
+    // some waves of that, then four (nvfp4, one / two / four: 999 x 2891 4.5 /
+    // 5.0 / 6.7 us, 2048 x 4096 7.2 / 6.2 / 6.9 us, 8192 x 4096 23.0 / 18.8 /
+    // 17.3 us); no more than a row has for a warp.
+    const long long total = a.rows * chunks;
+    if (chunks <= 32 || (chunks <= 512 && total <= 1350ll * sm_count())) return run_quantize<T, NV, 1>(a, threads(1), stream);
+    if (chunks <= 64 || (chunks <= 1024 && total <= 7000ll * sm_count())) return run_quantize<T, NV, 2>(a, threads(2), stream);
     return run_quantize<T, NV, 4>(a, threads(4), stream);
 }
 
