@@ -62,7 +62,7 @@ struct WideParams {
 template <bool NV, int kHalves>
 struct WideSmem {
     static constexpr int kUnits = NV ? 4 : 2;
-    static constexpr int kCols = kHalves == 1 && !NV ? 224 : 192;  // columns of an accumulator
+    static constexpr int kCols = kHalves == 1 ? 224 : 192;  // columns of an accumulator
     // scales in tensor memory: the weight's, then each half's, in one or two sets
     static constexpr uint32_t kScaleCols = 2 * kCols, kScaleSet = (4 + 8 * kHalves) * kUnits;
     static constexpr int kSets = kScaleCols + 2 * kScaleSet <= 512 ? 2 : 1;
@@ -465,7 +465,6 @@ mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     int best = 0;
     double least = 0;
     for (int TT : {384, 320, 256, 224, 192, 160, 128, 96, 64, 32}) {
-        if (nv && TT == 224) continue;  // more than its accumulators
         const bool two = TT > 224;
         const double even = static_cast<double>((x.rows + mats * TT - 1) / (mats * TT)) * mats;
         const double tiles = (mats == 1 ? even : std::max<double>(mats, static_cast<double>(x.rows) / TT + 0.5 * mats)) * NT;

@@ -754,10 +754,11 @@ class Fp4Weight:
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
-    def _quantized(self, X: Fp4Tensor, dtype):
+    def _quantized(self, X: Fp4Tensor, dtype, Y):
         if X.fmt != self.fmt or X.K != self.K or X._index != self._index:
             raise ValueError(f"the activations must be {self.fmt} with K = {self.K} on {self.device}")
-        dtype = _t.bf16 if dtype is None else dtype
+        if dtype is None:
+            dtype = _t.bf16 if Y is None else Y.dtype
         return dtype, _dtype(dtype, "the output")
 
     def _input(self, X, dtype):
@@ -777,13 +778,13 @@ class Fp4Weight:
     def linear(self, X, Y=None, workspace=None, *, dtype=None, stream=None):
         """Y = X @ W^T. X: a bf16 or fp16 [M, K] tensor, quantised within the
         call into the workspace (workspace_bytes(M) bytes), with Y of its
-        type; or an Fp4Tensor, with Y of `dtype` (bf16 unless given)."""
+        type; or an Fp4Tensor, with Y of `dtype` (Y's own or bf16 unless given)."""
         index = self._index
         if _elsewhere(index, stream):
             with _On(index, stream):
                 return self.linear(X, Y, workspace, dtype=dtype)
         if isinstance(X, Fp4Tensor):
-            dtype, d = self._quantized(X, dtype)
+            dtype, d = self._quantized(X, dtype, Y)
             Y, ldy = self._output(Y, X.rows, dtype)
             st = _lib.mq_fp4_linear_codes(self._h, *X._at, X.rows, Y.data_ptr(), d, ldy, _t.raw_stream(index))
             if st:
@@ -814,7 +815,7 @@ class Fp4Weight:
         if isinstance(X, Fp4Tensor):
             if rows is not None:
                 raise ValueError("rows are taken when X is quantised: fp4_quantize(X, rows=rows)")
-            dtype, d = self._quantized(X, dtype)
+            dtype, d = self._quantized(X, dtype, Y)
             Y, ldy = self._output(Y, X.rows, dtype)
             st = _lib.mq_fp4_linear_grouped_codes(self._h, *X._at, X.rows, offsets.data_ptr(), Y.data_ptr(), d,
                                                   ldy, _t.raw_stream(index))

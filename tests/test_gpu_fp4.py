@@ -152,7 +152,8 @@ def test_dequantize_types_and_strides(mq, cuda, fmt, dtype, M, K):
 # ---------------------------------------------------------------- linear
 LINEAR = [(1, 1, 1), (1, 128, 256), (1, 4096, 512), (2, 130, 64), (16, 128, 2048), (17, 300, 1001), (7, 1111, 32),
           (33, 257, 4100), (64, 640, 768), (65, 127, 300), (128, 128, 256), (129, 384, 1280), (250, 260, 515),
-          (513, 200, 96), (1025, 512, 512)]
+          (513, 200, 96), (1025, 512, 512), (3, 300, 1536), (5, 260, 1792), (40, 200, 1280), (50, 256, 1792),
+          (12, 512, 700), (16, 384, 5000)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -167,6 +168,7 @@ def test_linear(mq, cuda, fmt, dtype, M, N, K):
     assert torch.equal(w.linear(X.to(cuda)), Y)  # no dependence on timing
     q = mq.fp4_quantize(X.to(cuda), fmt)
     assert torch.equal(w.linear(q, dtype=dtype), Y)
+    assert torch.equal(w.linear(q, torch.empty_like(Y)), Y)
     assert w.device_error() == 0
 
 
@@ -369,7 +371,95 @@ def test_refusals(mq, cuda):
     torch.cuda.synchronize()
 
 
+# ---------------------------------------------------------------- sizes past 32 bits
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(mq, cuda, fmt):
+    # X and Y of more than 2^32 bytes and 2^31 elements; only some rows are
+    # not zeros
+    M, N, K = 66000, 33000, 64
+    X = torch.zeros(M, K, dtype=BF16, device=cuda)
+    rows = torch.tensor([0, 40000, M - 1])
+    X[rows] = values(3, K, BF16, 1, spread=0.3).to(cuda)
+    W = values(N, K, BF16, 2, spread=0.3)
+    w = mq.Fp4Weight.pack(W.to(cuda), fmt)
+    Y = w.linear(X)
+    assert Y.numel() > 2**31
+    check_product(Y[rows.to(cuda)], held(X[rows.to(cuda)], fmt), held(W, fmt), BF16)
+    live = torch.zeros(M, dtype=torch.bool, device=cuda)
+    live[rows.to(cuda)] = True
+    assert not Y[~live].any() and w.device_error() == 0
+    del X, Y, live
+    M, K = 140000, 32768
+    X = torch.zeros(M, K, dtype=BF16, device=cuda)
+    rows = torch.tensor([0, 65537, 131075, M - 1], device=cuda)
+    X[rows] = values(4, K, BF16, 3).to(cuda)
+    q = mq.fp4_quantize(X, fmt)
+    assert X.numel() * 2 > 2**32 and q.codes.numel() > 2**31
+    c, s, r = fp4.quantize(X[rows].float().cpu().numpy(), fmt)
+    cb, sb = fp4.pack(c, s, fmt)
+    assert np.array_equal(q.codes[rows].cpu().numpy(), cb) and np.array_equal(q.scales[rows].cpu().numpy(), sb)
+    Y = q.dequantize(BF16)
+    assert torch.equal(Y[rows], mq.fp4_quantize(X[rows], fmt).dequantize(BF16))
+
+
 # ---------------------------------------------------------------- streams, graphs, layers
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 9, 40, 300])
+def test_chain_without_waits(mq, cuda, fmt, M):
+    # layers whose launches overlap: the same bits as one launch at a time,
+    # with inputs that torch kernels write right before and overwrite right after
+    D = 512
+    ws = [mq.Fp4Weight.pack((values(D, D, BF16, k, spread=0.1) * 0.05).to(cuda), fmt) for k in range(6)]
+    experts = mq.Fp4Weight.pack((values(4 * D, D, BF16, 9, spread=0.1) * 0.05).view(4, D, D).to(cuda), fmt)
+    offsets = torch.tensor([0, M // 3, M // 3, M, M], dtype=torch.int32, device=cuda)
+    start = values(M, D, BF16, 7, spread=0.2).to(cuda)
+
+    def run(wait):
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        x, seen = start.clone(), []
+        for step in range(8):
+            for w in ws:
+                y = w.linear(x)
+                sync()
+                x.copy_(y)
+                sync()
+            off = offsets.clone()
+            y = experts.linear_grouped(x, off)
+            sync()
+            off.zero_()
+            q = mq.fp4_quantize(y, fmt)
+            sync()
+            y.zero_()
+            y = ws[0].linear(q)
+            sync()
+            seen.append(q.dequantize(BF16))
+            x.copy_(y).mul_(0.5).add_(start)
+            sync()
+        torch.cuda.synchronize()
+        return seen + [x]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_beside_the_other_linears(mq, cuda, fmt):
+    # this library's other products before and after on one stream, whose
+    # launches overlap with these
+    W = values(512, 512, FP32, 1, spread=0.1) * 0.05
+    a, b = mq.Weight.pack(W.numpy(), 0.01), mq.Fp4Weight.pack(W.to(cuda), fmt)
+    X = values(8, 512, BF16, 2, spread=0.2).to(cuda)
+
+    def run(sync):
+        x = X
+        for _ in range(6):
+            for f in (a.linear, b.linear, a.linear_w4a4, b.linear, b.linear):
+                x = f(x)
+                sync()
+        torch.cuda.synchronize()
+        return x
+
+    assert torch.equal(run(torch.cuda.synchronize), run(lambda: None))
 @pytest.mark.parametrize("fmt", FMTS)
 def test_other_stream(mq, cuda, fmt):
     w = mq.Fp4Weight.pack(values(300, 256, BF16, 1).to(cuda), fmt)
