@@ -26,12 +26,30 @@ constexpr int64_t fp4_scale_pitch(int fmt, int64_t K) {
     return (K + cols - 1) / cols * 16;
 }
 
-// A quantised matrix in caller memory (row-major codes and scales).
+// Token scales in the order the wide form takes them: slots of HT tokens of
+// one matrix, [slots][KS][units of four scale columns][unit bytes], a token's
+// four bytes at (x / 128) * 512 + (x % 32) * 16 + (x / 32 % 4) * 4 of each
+// unit for the slot's token x. Matrix e's tokens begin at row a = offsets[e],
+// and at slot a / HT + e: past every slot of the matrices before it, since
+// ceil(c / HT) <= floor((a + c) / HT) - floor(a / HT) + 1.
+struct Fp4Order {
+    int HT = 0;  // 0: row-major scales
+    int unit = 0;
+    int KS = 0;
+    int64_t slots = 0;
+    const int32_t *offsets = nullptr;  // NULL: one matrix with every row
+    int E = 1;
+    int64_t bytes(int fmt) const { return slots * KS * (fp4_stage_scales(fmt) / 4) * unit; }
+};
+
+// A quantised matrix in caller memory (row-major codes; scales row-major or
+// ordered).
 struct Fp4Rows {
     const uint8_t *codes;
     const uint8_t *scales;
     const float *row_scale;  // NULL for MQ_FP4_MX
     int64_t rows;
+    Fp4Order order;
 };
 
 // Device side of a packed weight: E matrices [N][K] of one format. A matrix is
@@ -67,7 +85,8 @@ constexpr int fp4_piece(int fmt) { return kFp4CodePiece + fp4_scale_piece(fmt); 
 // anything but packed weights).
 mq_status launch_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64_t K, int64_t ldx,
                               const int32_t *index, int64_t x_rows, int fmt, uint8_t *codes,
-                              uint8_t *scales, float *row_scale, bool open, cudaStream_t stream);
+                              uint8_t *scales, float *row_scale, const Fp4Order &order, bool open,
+                              cudaStream_t stream);
 
 mq_status launch_fp4_dequantize(const Fp4Rows &x, int64_t K, int fmt, void *Y, mq_dtype dtype,
                                 int64_t ldy, cudaStream_t stream);
@@ -89,7 +108,16 @@ mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype d
                                    const int32_t *index, int64_t x_rows, const int32_t *offsets, void *Y,
                                    int64_t ldy, cudaStream_t stream);
 
-// The form of launch_fp4_linear for many tokens (fp4_wide.cu).
+// The order in which launch_fp4_linear wants the scales of `rows` rows that
+// are quantised for it.
+Fp4Order fp4_token_order(const Fp4Device &d, int64_t rows, const int32_t *offsets);
+
+// The form of launch_fp4_linear for many tokens (fp4_wide.cu): the tokens of
+// a tile and the halves they come in.
+struct Fp4WidePlan {
+    int TT, halves;
+};
+Fp4WidePlan fp4_wide_plan(const Fp4Device &d, int64_t rows);
 mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                           mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
 

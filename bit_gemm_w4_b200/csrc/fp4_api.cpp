@@ -119,9 +119,9 @@ mq_status new_weight(mq_fp4_weight **out) {
 // The buffers of R quantised rows inside a workspace.
 struct Workspace {
     int64_t scales, factors, total;
-    Workspace(int64_t R, int64_t K, int fmt) {
+    Workspace(int64_t R, int64_t K, int fmt, const Fp4Order &order) {
         scales = R * fp4_code_pitch(K);
-        factors = scales + R * fp4_scale_pitch(fmt, K);
+        factors = scales + (order.HT ? order.bytes(fmt) : R * fp4_scale_pitch(fmt, K));
         total = factors + (fmt == MQ_FP4_NV ? (R * 4 + 15) / 16 * 16 : 0);
     }
 };
@@ -155,7 +155,8 @@ mq_status quantize_and_multiply(const mq_fp4_weight *w, const void *X, int dtype
         if (mq_status st = check_device(w)) return st;
         return launch_fp4_linear_direct(d, X, static_cast<mq_dtype>(dtype), R, ldx, index, x_rows, offsets, Y, ldy, s);
     }
-    const Workspace ws(R, d.K, d.fmt);
+    const Fp4Order order = fp4_token_order(d, R, offsets);
+    const Workspace ws(R, d.K, d.fmt, order);
     if (!workspace || !aligned16(workspace)) return fail(MQ_ERR_INVALID_ARG, "the workspace is NULL or not 16-byte aligned");
     if (workspace_bytes < static_cast<size_t>(ws.total))
         return fail(MQ_ERR_INVALID_ARG, "workspace smaller than mq_fp4_workspace_bytes");
@@ -163,9 +164,9 @@ mq_status quantize_and_multiply(const mq_fp4_weight *w, const void *X, int dtype
     uint8_t *base = static_cast<uint8_t *>(workspace);
     float *factors = d.fmt == MQ_FP4_NV ? reinterpret_cast<float *>(base + ws.factors) : nullptr;
     if (mq_status st = launch_fp4_quantize(X, static_cast<mq_dtype>(dtype), R, d.K, ldx, index, x_rows, d.fmt, base,
-                                           base + ws.scales, factors, offsets == nullptr, s))
+                                           base + ws.scales, factors, order, offsets == nullptr, s))
         return st;
-    const Fp4Rows x{base, base + ws.scales, factors, R};
+    const Fp4Rows x{base, base + ws.scales, factors, R, order};
     return launch_fp4_linear(d, x, offsets, Y, static_cast<mq_dtype>(dtype), ldy, true, s);
 }
 
@@ -177,7 +178,7 @@ mq_status multiply(const mq_fp4_weight *w, const void *codes, const void *scales
     if (mq_status st = check_quantized(codes, scales, row_scale, w->d.fmt)) return st;
     if (mq_status st = check_output(w, Y, dtype, ldy)) return st;
     if (mq_status st = check_device(w)) return st;
-    const Fp4Rows x{static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), row_scale, R};
+    const Fp4Rows x{static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), row_scale, R, {}};
     return launch_fp4_linear(w->d, x, offsets, Y, static_cast<mq_dtype>(dtype), ldy, false,
                              reinterpret_cast<cudaStream_t>(stream));
 }
@@ -211,7 +212,7 @@ mq_status mq_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64_t K
     if (rows == 0) return MQ_OK;
     if (mq_status st = check_quantized(codes, scales, row_scale, fmt)) return st;
     return launch_fp4_quantize(X, dtype, rows, K, ldx, index, x_rows, fmt, static_cast<uint8_t *>(codes),
-                               static_cast<uint8_t *>(scales), row_scale, true, reinterpret_cast<cudaStream_t>(stream));
+                               static_cast<uint8_t *>(scales), row_scale, {}, true, reinterpret_cast<cudaStream_t>(stream));
 }
 
 mq_status mq_fp4_dequantize(const void *codes, const void *scales, const float *row_scale, int64_t rows, int64_t K,
@@ -227,7 +228,7 @@ mq_status mq_fp4_dequantize(const void *codes, const void *scales, const float *
     if (reinterpret_cast<uintptr_t>(Y) & (dtype == MQ_FP32 ? 3 : 1))
         return fail(MQ_ERR_INVALID_ARG, "Y is not aligned to its elements");
     if (ldy < K || ldy > (int64_t(1) << 40)) return fail(MQ_ERR_INVALID_ARG, "ldy is smaller than K or too large");
-    const Fp4Rows x{static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), row_scale, rows};
+    const Fp4Rows x{static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), row_scale, rows, {}};
     return launch_fp4_dequantize(x, K, fmt, Y, dtype, ldy, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -296,7 +297,7 @@ mq_status mq_fp4_pack(const void *W, mq_dtype dtype, int64_t E, int64_t N, int64
     }
     if (!st)
         st = launch_fp4_quantize(W, dtype, E * N, K, K, nullptr, E * N, fmt, rows, rows + code_bytes, w->d.row_scale,
-                                 false, s);
+                                 {}, false, s);
     if (!st) st = launch_fp4_order(w->d, rows, rows + code_bytes, false, s);
     if (rows) {
         e = cudaStreamSynchronize(s);
@@ -338,7 +339,7 @@ mq_status mq_fp4_export(const mq_fp4_weight *w, void *codes, void *scales, float
 
 int64_t mq_fp4_workspace_bytes(const mq_fp4_weight *w, int64_t rows) {
     if (!w || rows <= 0 || rows > kMaxRows || fp4_linear_quantises(w->d, rows)) return 0;
-    return Workspace(rows, w->d.K, w->d.fmt).total;
+    return Workspace(rows, w->d.K, w->d.fmt, fp4_token_order(w->d, rows, nullptr)).total;
 }
 
 mq_status mq_fp4_linear(const mq_fp4_weight *w, const void *X, mq_dtype dtype, int64_t M, int64_t ldx, void *Y,

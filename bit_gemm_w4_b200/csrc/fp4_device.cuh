@@ -61,6 +61,7 @@ __device__ __forceinline__ uint2 load_u64(const void *p) {
 // together) over ascending tile indices.
 struct Tile {
     int e, m0, tokens, nt;
+    int first;  // the matrix's first row
 };
 
 struct TileWalk {
@@ -77,7 +78,7 @@ struct TileWalk {
             const int tiles = (R + TT - 1) / TT;
             if (t >= static_cast<long long>(tiles) * NT) return false;
             const int tt = static_cast<int>(t % tiles);
-            out = {0, tt * TT, min(TT, R - tt * TT), static_cast<int>(t / tiles)};
+            out = {0, tt * TT, min(TT, R - tt * TT), static_cast<int>(t / tiles), 0};
             return true;
         }
         const int lane = threadIdx.x & 31;
@@ -104,7 +105,7 @@ struct TileWalk {
                 const long long within = t - before - __shfl_sync(0xffffffffu, sum - mine, l);
                 const int tiles = (b - a + TT - 1) / TT;
                 const int tt = static_cast<int>(within % tiles);
-                out = {base + l, a + tt * TT, min(TT, b - a - tt * TT), static_cast<int>(within / tiles)};
+                out = {base + l, a + tt * TT, min(TT, b - a - tt * TT), static_cast<int>(within / tiles), a};
                 return true;
             }
             before += __shfl_sync(0xffffffffu, sum, 31);

@@ -28,6 +28,7 @@ struct QuantArgs {
     long long rows;
     long long cpitch, spitch;  // bytes of a row of codes, of scales
     RowSource from;
+    Fp4Order order;
     bool open;
 };
 
@@ -74,6 +75,25 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
         if (x >= 0 && x < a.x_rows) src = static_cast<const T *>(a.X) + x * a.ldx;
     }
     const bool aligned = (reinterpret_cast<uintptr_t>(src) & 31) == 0;
+    // where the row's scales go
+    uint8_t *scales = a.scales + r * a.spitch;
+    if (a.order.HT) {
+        long long slot = r / a.order.HT, x = r % a.order.HT;
+        if (a.order.offsets && real) {
+            // the last matrix that begins at or before the row
+            int e = -1;
+            for (int i = tx & 31; i - (tx & 31) < a.order.E; i += 32) {
+                const bool before = i < a.order.E && min(max(load_i32(a.order.offsets + i), 0), static_cast<int>(a.rows)) <= r;
+                e += __popc(__ballot_sync(0xffffffffu, before));
+            }
+            const int first = e < 0 ? 0 : min(max(load_i32(a.order.offsets + e), 0), static_cast<int>(a.rows));
+            slot = e < 0 ? -1 : first / a.order.HT + e + (r - first) / a.order.HT;
+            x = (r - first) % a.order.HT;
+        }
+        scales = !real || slot < 0 ? nullptr
+                                   : a.scales + slot * a.order.KS * (NV ? 4 : 2) * a.order.unit + (x >> 7) * 512 +
+                                         (x & 31) * 16 + ((x >> 5) & 3) * 4;
+    }
     auto load_one = [&](Raw<T> &t, int ch) {
         if (src && aligned && ch < whole_chunks)
             load_whole_chunk(t, src + ch * kChunk);
@@ -113,7 +133,7 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
         if (tx == 0 && real) a.row_scale[r] = factor;
     }
 
-    uint8_t *codes = a.codes + r * a.cpitch, *scales = a.scales + r * a.spitch;
+    uint8_t *codes = a.codes + r * a.cpitch;
     for (int base = 0; base < chunks; base += step) {
         if (base > 0) load(base);
 #pragma unroll
@@ -128,9 +148,20 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 scale = mx_scale<T>(top, inv);
             }
+            if (ch >= real_chunks) scale = 0;
+            if (a.order.HT) {
+                // four scales of a row are a word: 4 lanes' (8 lanes' of MQ_FP4_MX)
+                constexpr int kLanes = NV ? 4 : 8;
+                uint32_t word = scale << (8 * (NV ? tx & 3 : (tx >> 1) & 3));
+                word |= __shfl_xor_sync(0xffffffffu, word, kLanes / 4);
+                word |= __shfl_xor_sync(0xffffffffu, word, kLanes / 2);
+                const int unit = ch / kLanes;  // units of a stage follow one another
+                if (scales && (tx & (kLanes - 1)) == 0 && unit < a.order.KS * (NV ? 4 : 2))
+                    *reinterpret_cast<uint32_t *>(scales + static_cast<long long>(unit) * a.order.unit) = word;
+            }
             if (!real || ch >= chunks) continue;
             if (ch < code_chunks) *reinterpret_cast<uint2 *>(codes + ch * 8) = codes_of(raw[j], inv);
-            if (ch >= real_chunks) scale = 0;
+            if (a.order.HT) continue;
             if constexpr (NV)
                 scales[ch] = static_cast<uint8_t>(scale);
             else if ((ch & 1) == 0)
@@ -351,11 +382,13 @@ __global__ void __launch_bounds__(256) fp4_order_kernel(uint8_t *pieces, uint8_t
 
 mq_status launch_fp4_quantize(const void *X, mq_dtype dtype, int64_t rows, int64_t K, int64_t ldx,
                               const int32_t *index, int64_t x_rows, int fmt, uint8_t *codes,
-                              uint8_t *scales, float *row_scale, bool open, cudaStream_t stream) {
+                              uint8_t *scales, float *row_scale, const Fp4Order &order, bool open,
+                              cudaStream_t stream) {
     if (rows <= 0) return MQ_OK;
     const int64_t size = dtype == MQ_FP32 ? 4 : 2;
     QuantArgs a{X, ldx, x_rows, index, codes, scales, row_scale, rows, fp4_code_pitch(K), fp4_scale_pitch(fmt, K),
-                {K, static_cast<const char *>(X), static_cast<const char *>(X) + ((x_rows - 1) * ldx + K) * size}, open};
+                {K, static_cast<const char *>(X), static_cast<const char *>(X) + ((x_rows - 1) * ldx + K) * size}, order,
+                open};
     const bool nv = fmt == MQ_FP4_NV;
     switch (dtype) {
         case MQ_BF16: return nv ? pick_quantize<__nv_bfloat16, true>(a, stream) : pick_quantize<__nv_bfloat16, false>(a, stream);

@@ -16,11 +16,11 @@
 // 30 %, and the epilogue packs its outputs into registers first, so that the
 // next tile waits for that alone and not for the stores.
 //
-// Each CTA fills its own ring: warp 0 copies codes and weight scales (TMA),
-// warps 2 to 5 place all the tile's token scales (row-major in memory) in the
-// tensor core's order; both report to the first CTA's barriers, whose warp 1
-// issues scale copies to tensor memory and MMAs for the pair. Warps 6 to 13
-// are the epilogue.
+// Each CTA fills its own ring: warp 0 copies codes and scales (TMA). Token
+// scales that lie row by row in memory (tokens the caller quantised) are
+// placed in the tensor core's order by warps 2 to 5 instead. Both report to
+// the first CTA's barriers, whose warp 1 issues scale copies to tensor memory
+// and MMAs for the pair. Warps 6 to 13 are the epilogue.
 
 #include <algorithm>
 #include <cmath>
@@ -41,6 +41,7 @@ constexpr int kLoaders = 4;
 
 struct WideParams {
     CUtensorMap tw, tx, tx_small;  // boxes of a piece of the weight, half a MMA's tokens, 16 tokens
+    CUtensorMap tsx;               // ordered token scales, a slot's stage a box
     const float *wfactor;
     const uint8_t *xscales;
     const float *xfactor;
@@ -57,6 +58,7 @@ struct WideParams {
     int fp16;
     int paired;  // N, the stride and Y's address are even: 4-byte stores
     int wait_first;
+    int ordered;
 };
 
 template <bool NV, int kHalves>
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&full[s], 1 + 2 * kLoaders);  // the first CTA's producer, both CTAs' loaders
+            mbar_init(&full[s], p.ordered ? 1 : 1 + 2 * kLoaders);  // the first CTA's producer, both CTAs' loaders
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -125,10 +127,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
         int s = 0, ph = 1, first = 1;
         bool ok = true;
         for (long long ti = pair; ok && walk.find(ti, t); ti += pairs) {
-            int columns = 0;
+            uint32_t bytes = 2 * S::kPiece;  // both CTAs' copies
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) columns += cols_of(t, h);
-            const uint32_t bytes = 2 * S::kPiece + columns * 128;  // both CTAs' copies
+            for (int h = 0; h < kHalves; ++h) {
+                const int n = cols_of(t, h);
+                bytes += n * 128 + (p.ordered && n ? 2 * kUnits * unit : 0);
+            }
+            const int token_slot = (p.offsets ? t.first / HT + t.e : 0) + (t.m0 - t.first) / HT;
             // past the last row tile (an odd count) that tile again: rows that are not stored
             const int nt1 = min(t.nt * 2 + static_cast<int>(rank), p.NT1 - 1);
             const int piece = (t.e * p.NT1 + nt1) * KS;
@@ -143,6 +148,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
                 for (int h = 0; h < kHalves; ++h) {
                     uint8_t *at = smem + slot_i * slot + at_b + h * HT * 64;
                     const int half = cols_of(t, h) / 2, m = t.m0 + h * HT + rank * half;
+                    if (half == 0) break;
+                    if (p.ordered)
+                        tma_pair_load_2d(smem + slot_i * slot + at_sb + h * kUnits * unit, &p.tsx, bar, 0,
+                                         ((token_slot + h) * KS + k) * (kUnits * unit / 128));
                     if (half == HT / 2)
                         tma_pair_load_2d(at, &p.tx, bar, k * 128, m);
                     else
@@ -229,6 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
             ok = __all_sync(0xffffffffu, ok);
             if (++b == kBuffers) b = 0, bph ^= 1;
         }
+    } else if (warp < 6 && p.ordered) {
+        // nothing to place
     } else if (warp < 6) {
         // the tokens' scales, two stages at a time: a row's 32 (MQ_FP4_MX: 16)
         // bytes are read in one go, one pair of stages ahead of their turn
@@ -411,6 +422,9 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activations");
     p.paired = d.N % 2 == 0 && ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(Y) & 3) == 0;
     p.wfactor = d.row_scale;
+    p.ordered = x.order.HT != 0;
+    if (p.ordered && !encode_bytes_map(&p.tsx, x.scales, 128, x.order.bytes(d.fmt) / 128, S::kUnits * x.order.unit / 128, false))
+        return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the activations' scales");
     p.xscales = x.scales;
     p.xfactor = x.row_scale;
     p.offsets = offsets;
@@ -450,34 +464,40 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     return MQ_OK;
 }
 
-mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,
-                          int64_t ldy, bool chained, cudaStream_t stream) {
+Fp4WidePlan fp4_wide_plan(const Fp4Device &d, int64_t rows) {
     // Tokens of a tile: the choice that leaves the least time over the waves of
     // tiles. A stage takes a time that does not depend on the tokens plus one
     // for each of them; the constants (ns) fit 8192^3, 4096 x 4096 x 11008 and
     // 2048 x 14336 x 4096 at 128 to 384 tokens, all of which run at the power
     // limit. Two halves move less and pay 1 us a tile, for which K has to be
-    // long: 4096 x 4096 x 11008 mxfp4 takes 76 us with 320 tokens and 82 us
-    // with 192, 2048 x 14336 x 4096 nvfp4 84 us with 384 and 73 us with 192.
+    // long: 8192^3 mxfp4 takes 274 us with 384 tokens and 291 us with 224, 2048
+    // x 14336 x 4096 nvfp4 85 and 76 us (both with the quantisation).
     // Matrices of a ragged batch end half a tile early on average.
     const bool nv = d.fmt == MQ_FP4_NV;
-    const int64_t NT = (d.NT + 1) / 2, pairs = d.sms / 2, mats = std::min<int64_t>(d.E, x.rows);
+    const int64_t NT = (d.NT + 1) / 2, pairs = d.sms / 2, mats = std::min<int64_t>(d.E, rows);
     int best = 0;
     double least = 0;
     for (int TT : {384, 320, 256, 224, 192, 160, 128, 96, 64, 32}) {
         const bool two = TT > 224;
-        const double even = static_cast<double>((x.rows + mats * TT - 1) / (mats * TT)) * mats;
-        const double tiles = (mats == 1 ? even : std::max<double>(mats, static_cast<double>(x.rows) / TT + 0.5 * mats)) * NT;
+        const double even = static_cast<double>((rows + mats * TT - 1) / (mats * TT)) * mats;
+        const double tiles = (mats == 1 ? even : std::max<double>(mats, static_cast<double>(rows) / TT + 0.5 * mats)) * NT;
         double waves = tiles / pairs;
         if (mats == 1 || waves < 1) waves = std::ceil(waves);
-        const double stage = nv ? (two ? 200 + 1.67 * TT : 210 + 1.35 * TT) : (two ? 260 + 0.96 * TT : 245 + 0.66 * TT);
+        const double stage = nv ? (two ? 200 + 1.67 * TT : 210 + 1.35 * TT) : (two ? 240 + 0.9 * TT : 245 + 0.66 * TT);
         const double cost = waves * (d.KS * stage + (two ? 1000 : 0));
         if (!best || cost < least) least = cost, best = TT;
     }
-    if (best > 224) return nv ? run_wide<true, 2>(d, x, offsets, Y, dtype, ldy, chained, stream, best)
-                              : run_wide<false, 2>(d, x, offsets, Y, dtype, ldy, chained, stream, best);
-    return nv ? run_wide<true, 1>(d, x, offsets, Y, dtype, ldy, chained, stream, best)
-              : run_wide<false, 1>(d, x, offsets, Y, dtype, ldy, chained, stream, best);
+    return {best, best > 224 ? 2 : 1};
+}
+
+mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,
+                          int64_t ldy, bool chained, cudaStream_t stream) {
+    const Fp4WidePlan plan = fp4_wide_plan(d, x.rows);
+    const bool nv = d.fmt == MQ_FP4_NV;
+    if (plan.halves == 2) return nv ? run_wide<true, 2>(d, x, offsets, Y, dtype, ldy, chained, stream, plan.TT)
+                                    : run_wide<false, 2>(d, x, offsets, Y, dtype, ldy, chained, stream, plan.TT);
+    return nv ? run_wide<true, 1>(d, x, offsets, Y, dtype, ldy, chained, stream, plan.TT)
+              : run_wide<false, 1>(d, x, offsets, Y, dtype, ldy, chained, stream, plan.TT);
 }
 
 }  // namespace mq
