@@ -53,7 +53,7 @@ cudaError_t launch_after(void (*kernel)(A), const A &args, dim3 grid, dim3 block
 // holds kChunks chunks of its row, all on their way from memory at once;
 // wider rows are read twice by MQ_FP4_NV, whose row factor needs the whole row
 // first.
-template <class T, bool NV, int kChunks>
+template <class T, bool NV, int kChunks, bool kOrdered>
 __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
     // The launch after this one starts early: at once when all it looks at
     // before its own wait is a packed weight, else when the launches before
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
     const bool aligned = (reinterpret_cast<uintptr_t>(src) & 31) == 0;
     // where the row's scales go
     uint8_t *scales = a.scales + r * a.spitch;
-    if (a.order.HT) {
+    if constexpr (kOrdered) {
         long long slot = r / a.order.HT, x = r % a.order.HT;
         if (a.order.offsets && real) {
             // the last matrix that begins at or before the row
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
                 scale = mx_scale<T>(top, inv);
             }
             if (ch >= real_chunks) scale = 0;
-            if (a.order.HT) {
+            if constexpr (kOrdered) {
                 // four scales of a row are a word: 4 lanes' (8 lanes' of MQ_FP4_MX)
                 constexpr int kLanes = NV ? 4 : 8;
                 uint32_t word = scale << (8 * (NV ? tx & 3 : (tx >> 1) & 3));
@@ -161,8 +161,9 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
             }
             if (!real || ch >= chunks) continue;
             if (ch < code_chunks) *reinterpret_cast<uint2 *>(codes + ch * 8) = codes_of(raw[j], inv);
-            if (a.order.HT) continue;
-            if constexpr (NV)
+            if constexpr (kOrdered)
+                continue;
+            else if constexpr (NV)
                 scales[ch] = static_cast<uint8_t>(scale);
             else if ((ch & 1) == 0)
                 scales[ch >> 1] = static_cast<uint8_t>(scale);
@@ -175,8 +176,14 @@ mq_status run_quantize(const QuantArgs &a, int bx, cudaStream_t stream) {
     const int by = std::max(1, 128 / bx);
     const long long grid = (a.rows + by - 1) / by;
     if (grid > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 quantisation: too many rows");
-    const cudaError_t e = launch_after(fp4_quantize_kernel<T, NV, kChunks>, a, dim3(static_cast<unsigned>(grid)),
-                                       dim3(bx, by), stream);
+    cudaError_t e = cudaSuccess;
+    if constexpr (sizeof(T) == 2)  // the products' types
+        if (a.order.HT)
+            e = launch_after(fp4_quantize_kernel<T, NV, kChunks, true>, a, dim3(static_cast<unsigned>(grid)), dim3(bx, by),
+                             stream);
+    if (!a.order.HT)
+        e = launch_after(fp4_quantize_kernel<T, NV, kChunks, false>, a, dim3(static_cast<unsigned>(grid)), dim3(bx, by),
+                         stream);
     if (e != cudaSuccess)
         return fail(MQ_ERR_CUDA, std::string("fp4 quantisation launch: ") + cudaGetErrorString(e));
     return MQ_OK;
