@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "fp4_convert.cuh"
 #include "tc5.cuh"
 
 namespace mq {
@@ -131,21 +132,34 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// v[j] * f[j] * w for sixteen tokens, each product rounded; f: 16 bytes aligned.
+__device__ __forceinline__ void apply_factors(float (&v)[16], const float *f, float w) {
+    const uint64_t w2 = pack2(w, w);
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        const ulonglong2 g = *reinterpret_cast<const ulonglong2 *>(f + j);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            uint64_t d;
+            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(v[j + i], v[j + i + 1])), "l"(i ? g.y : g.x));
+            asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(w2));
+            v[j + i] = __uint_as_float(static_cast<uint32_t>(d));
+            v[j + i + 1] = __uint_as_float(static_cast<uint32_t>(d >> 32));
+        }
+    }
+}
+
 // Sixteen tokens' outputs of this lane's weight row, as 16-bit words ready to
 // be stored. With `paired` (N, ldy and Y's address even) neighbouring lanes
 // trade halves: even lanes then hold two rows of the even tokens, odd lanes
 // two rows of the odd ones, 4 bytes a lane and two tokens a warp's store;
 // without, a word holds two tokens of the lane's own row. Called by whole warps.
 __device__ __forceinline__ void pack_chunk(const float (&v)[16], uint32_t (&w)[8], bool paired, bool fp16) {
-    const bool odd = threadIdx.x & 1;
+    const uint32_t pick = threadIdx.x & 1 ? 0x3276u : 0x5410u;
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
         const uint32_t mine = fp16 ? pack_f16(v[j], v[j + 1]) : pack_bf16(v[j], v[j + 1]);
-        w[j / 2] = mine;
-        if (paired) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-            w[j / 2] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-        }
+        w[j / 2] = paired ? __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick) : mine;
     }
 }
 

@@ -402,12 +402,9 @@ __global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_const
                 continue;
             }
             float v[16];
-            const float fw = NV ? wfactors[row] : 1.0f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                v[j] = __uint_as_float(bits[j]);
-                if constexpr (NV) v[j] = v[j] * factors[c + j] * fw;
-            }
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(bits[j]);
+            if constexpr (NV) apply_factors(v, factors + c, wfactors[row]);
             store_chunk(v, p.Y, p.ldy, m0 + c, n, left, n < p.N, p.paired, p.fp16);
         }
     }

@@ -335,16 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
             auto outputs = [&](const uint32_t (&bits)[16], int c, float (&v)[16]) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(bits[j]);
-                if constexpr (NV) {
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(factors + c + j);
-                        v[j] = v[j] * f.x * fw;
-                        v[j + 1] = v[j + 1] * f.y * fw;
-                        v[j + 2] = v[j + 2] * f.z * fw;
-                        v[j + 3] = v[j + 3] * f.w * fw;
-                    }
-                }
+                if constexpr (NV) apply_factors(v, factors + c, fw);
             };
             auto release = [&] {
                 tc5::fence_before();
