@@ -83,7 +83,7 @@ struct NarrowSmem {
 
 // T: void for tokens quantised before, else their type.
 template <bool NV, class T>
-__global__ void __launch_bounds__(kThreads) fp4_narrow_kernel(const __grid_constant__ NarrowParams p) {
+__global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_constant__ NarrowParams p) {
     using S = NarrowSmem<NV>;
     constexpr bool kQuantise = !std::is_same<T, void>::value;
     constexpr int kUnits = S::kUnits;
