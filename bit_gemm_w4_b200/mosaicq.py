@@ -533,10 +533,13 @@ class _On:
 
 def _rows_view(X, where: str):
     """A 2-D tensor whose rows are contiguous, its sizes and row stride."""
-    if X.dim() != 2 or X.shape[1] < 1:
+    shape = X.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError(f"{where}: a 2-D tensor with at least one column is needed")
-    M, K = X.shape
+    M, K = shape
     ld, one = X.stride()
+    if M > 1 and one == 1 and ld >= K:
+        return X, M, K, ld
     if (one != 1 and K > 1) or (ld < K and M > 1):
         X, ld = X.contiguous(), K
     return X, M, K, (ld if M > 1 else K)
@@ -586,12 +589,18 @@ class Fp4Tensor:
         scales and row_scale are views."""
         q = cls.__new__(cls)
         codes, scales = _row_bytes(K, fmt)
-        cut = rows * codes, rows * (codes + scales)
-        q._buffer = b = _t.empty(cut[1] + (4 * rows if fmt == "nvfp4" else 0), dtype=_t.u8, device=device)
-        at = b.data_ptr()
-        q._at = at, at + cut[0], at + cut[1] if fmt == "nvfp4" else None
+        codes, scales = rows * codes, rows * scales
+        q.K, q.fmt, q.rows = K, fmt, rows
         q._codes = q._scales = q._row_scale = None
-        q.K, q.fmt, q.rows, q._index = K, fmt, rows, b.get_device()
+        if fmt == "nvfp4":
+            q._buffer = b = _t.empty(codes + scales + 4 * rows, dtype=_t.u8, device=device)
+            at = b.data_ptr()
+            q._at = at, at + codes, at + codes + scales
+        else:
+            q._buffer = b = _t.empty(codes + scales, dtype=_t.u8, device=device)
+            at = b.data_ptr()
+            q._at = at, at + codes, None
+        q._index = b.get_device()
         return q
 
     def _view(self, which: int):
@@ -630,14 +639,19 @@ class Fp4Tensor:
         index = self._index
         if index < 0:
             raise ValueError(f"a CUDA tensor is needed, not one on {self.device}")
-        if _elsewhere(index, stream):
+        if stream is not None or _t.current_device() != index:
             with _On(index, stream):
                 return self.dequantize(dtype)
-        dtype = _t.fp32 if dtype is None else dtype
-        d = _dtype(dtype, "dequantize", fp32=True)
+        if dtype is None:
+            dtype = _t.fp32
+        d = _t.dtypes.get(dtype)
+        if d is None:
+            _dtype(dtype, "dequantize", fp32=True)
         rows, K = self.rows, self.K
         Y = _t.empty((rows, K), dtype=dtype, device=self.device)
-        st = _lib.mq_fp4_dequantize(*self._at, rows, K, FP4_FORMATS[self.fmt], Y.data_ptr(), d, K, _t.raw_stream(index))
+        codes, scales, row_scale = self._at
+        st = _lib.mq_fp4_dequantize(codes, scales, row_scale, rows, K, 1 if row_scale else 0, Y.data_ptr(), d, K,
+                                    _t.raw_stream(index))
         if st:
             _check(st, "mq_fp4_dequantize")
         return Y
@@ -647,10 +661,14 @@ def fp4_quantize(X, fmt: str = "nvfp4", *, rows=None, stream=None) -> Fp4Tensor:
     """X [M, K] (bf16, fp16 or fp32, any row stride) as microscaled 4-bit
     floating point. With rows (1-D integer tensor) output row r is X[rows[r]],
     and zeros where rows[r] is no row of X."""
-    f = _fmt(fmt)
-    d = _dtype(X.dtype, "fp4_quantize", fp32=True)
-    index = _cuda_index(X)
-    if _elsewhere(index, stream):
+    f, d = FP4_FORMATS.get(fmt), _t.dtypes.get(X.dtype)
+    if f is None or d is None:
+        _fmt(fmt)
+        _dtype(X.dtype, "fp4_quantize", fp32=True)
+    index = X.get_device()
+    if index < 0:
+        _cuda_index(X)
+    if stream is not None or _t.current_device() != index:
         with _On(index, stream):
             return fp4_quantize(X, fmt, rows=rows)
     X, M, K, ldx = _rows_view(X, "fp4_quantize")
@@ -659,7 +677,8 @@ def fp4_quantize(X, fmt: str = "nvfp4", *, rows=None, stream=None) -> Fp4Tensor:
         rows = _index(rows, index, "rows")
         R, at = rows.shape[0], rows.data_ptr()
     q = Fp4Tensor.empty(R, K, fmt, X.device)
-    st = _lib.mq_fp4_quantize(X.data_ptr(), d, R, K, ldx, at, M, f, *q._at, _t.raw_stream(index))
+    codes, scales, row_scale = q._at
+    st = _lib.mq_fp4_quantize(X.data_ptr(), d, R, K, ldx, at, M, f, codes, scales, row_scale, _t.raw_stream(index))
     if st:
         _check(st, "mq_fp4_quantize")
     return q
@@ -768,11 +787,7 @@ class Fp4Weight:
             raise ValueError("X must be bf16 or fp16, and Y has its type (dtype is for quantised activations)")
         if len(shape) != 2 or shape[1] != self.K or X.get_device() != self._index:
             raise ValueError(f"X must be a [rows, {self.K}] tensor on {self.device}")
-        M, K = shape
-        ld, one = X.stride()
-        if M > 1 and one == 1 and ld >= K:
-            return d, X, M, ld
-        X, _, _, ld = _rows_view(X, "X")
+        X, M, _, ld = _rows_view(X, "X")
         return d, X, M, ld
 
     def linear(self, X, Y=None, workspace=None, *, dtype=None, stream=None):
@@ -780,7 +795,7 @@ class Fp4Weight:
         call into the workspace (workspace_bytes(M) bytes), with Y of its
         type; or an Fp4Tensor, with Y of `dtype` (Y's own or bf16 unless given)."""
         index = self._index
-        if _elsewhere(index, stream):
+        if stream is not None or _t.current_device() != index:
             with _On(index, stream):
                 return self.linear(X, Y, workspace, dtype=dtype)
         if isinstance(X, Fp4Tensor):
@@ -806,7 +821,7 @@ class Fp4Weight:
         belong to no expert are left as they were (undefined in a Y that the
         call makes)."""
         index = self._index
-        if _elsewhere(index, stream):
+        if stream is not None or _t.current_device() != index:
             with _On(index, stream):
                 return self.linear_grouped(X, offsets, Y, workspace, rows=rows, dtype=dtype)
         offsets = _index(offsets, index, "offsets")
