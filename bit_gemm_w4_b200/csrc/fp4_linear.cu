@@ -62,8 +62,7 @@ struct NarrowParams {
 };
 
 // Shared memory: the ring (a piece of the weight, the tokens' codes and scales
-// in each slot),
-// partial sums from the cluster, the tokens' factors, barriers.
+// in each slot), partial sums from the cluster, factors, barriers.
 template <bool NV>
 struct NarrowSmem {
     static constexpr int kUnits = NV ? 4 : 2;  // 512-byte scale units of 128 rows in a stage
@@ -77,7 +76,9 @@ struct NarrowSmem {
     // Partial sums of up to 32 tokens have room of their own; more go where
     // the ring was, once every CTA of the cluster is done with it.
     __host__ __device__ static bool apart(int TT) { return TT <= 32; }
-    __host__ __device__ static int fixed(int TT, int split) { return (apart(TT) ? recv(TT, split) : 0) + kMaxTT * 12 + 512 + 256 + 1024; }
+    __host__ __device__ static int fixed(int TT, int split) {
+        return (apart(TT) ? recv(TT, split) : 0) + kMaxTT * 12 + 512 + 256 + 1024;
+    }
     __host__ __device__ static int total(int TT, int split, int stages) { return slot(TT) * stages + fixed(TT, split); }
 };
 
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_co
                 tma_load_2d(smem + s * slot + at_b + b * kBoxRows * 128, &p.tx, &full[s], (k0 + i) * 128,
                             m0 + b * kBoxRows);
         };
+        pdl_wait();  // the launch before may take its time: no wait with a limit before this
         if constexpr (!kQuantise) {
-            pdl_wait();
             if (tc5::elect())
                 for (int i = 0; i < ahead; ++i) tokens_in(i, i);
             __syncwarp();
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_co
         const uint32_t desc = tc5::idesc(128, nb * kBoxRows, !NV);
         const uint32_t sfa = tmem + TT, sfb = sfa + 4 * kUnits;
         bool ok = true;
-        pdl_wait();  // before any wait with a limit: the launch before may take its time
+        pdl_wait();  // as above
         for (int i = 0, s = 0, ph = 0; i < nk && ok; ++i) {
             ok = mbar_wait(&full[s], ph, p.err, kErrWaitFull, abort_flag);
             ok = __all_sync(0xffffffffu, ok);

@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_wide_kernel(const __grid_cons
         pdl_wait();  // before any wait with a limit: the launch before may take its time
         for (long long ti = pair; ok && walk.find(ti, t); ti += pairs) {
             ok = mbar_wait(&acc_empty[b], bph, p.err, kErrWaitEmpty, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
             for (int k = 0; k < KS && ok; ++k) {
                 ok = mbar_wait(&full[s], ph, p.err, kErrWaitFull, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);

@@ -193,6 +193,8 @@ def test_linear_large(mq, cuda, fmt, M, N, K):
     # bf16 (8 significant bits) is off by half a step, eps / 2 = 2^-8 of |y|
     tol = (torch.finfo(BF16).eps / 2 + 2**-21) * full.abs() + (K / 16 + K + 16) * 2.0**-23 * S + 2.0**-25
     assert ((Y.float() - full).abs() <= tol * 1.01).all()
+    # tokens quantised before, whose scales are row-major: the same bits
+    assert torch.equal(w.linear(mq.fp4_quantize(X.to(cuda), fmt)), Y)
     assert w.device_error() == 0
 
 
@@ -295,6 +297,17 @@ def grouped_check(mq, cuda, fmt, dtype, N, K, counts, lead=0, tail=0, index=None
 ])
 def test_grouped(mq, cuda, fmt, dtype, N, K, counts, lead, tail):
     grouped_check(mq, cuda, fmt, dtype, N, K, counts, lead, tail, seed=N)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("E,rows", [(300, 700), (2, 9000), (33, 5000)])
+def test_grouped_many(mq, cuda, fmt, E, rows):
+    # shares drawn at random, some of them empty, one of them half of all rows
+    g = np.random.default_rng(E)
+    cut = np.sort(g.integers(0, rows, E - 1))
+    counts = np.diff(np.concatenate([[0], cut, [rows]]))
+    counts[E // 2] += rows
+    grouped_check(mq, cuda, fmt, BF16, 72, 192, counts.tolist(), lead=5, tail=7, seed=E)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
