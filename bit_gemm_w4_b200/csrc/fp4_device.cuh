@@ -69,6 +69,7 @@ struct TileWalk {
     const int32_t *offsets;  // NULL: one matrix with all R rows
     int E, R, TT, NT;
     int base = 0;            // matrices [base, base + 32) hold the next tile, or later ones do
+    int top = 0;             // where the matrices below base end
     long long before = 0;    // tiles of the matrices below base
 
     __device__ __forceinline__ TileWalk(const int32_t *o, int e, int r, int tt, int nt)
@@ -85,11 +86,21 @@ struct TileWalk {
         const int lane = threadIdx.x & 31;
         while (base < E) {
             const int e = base + lane;
-            int a = 0, b = 0;
+            int a = R, b = R;
             if (e < E) {
-                // entries out of range or order are clamped, never followed
+                // entries out of range are clamped, never followed
                 a = min(max(load_i32(offsets + e), 0), R);
-                b = min(max(load_i32(offsets + e + 1), a), R);
+                b = min(max(load_i32(offsets + e + 1), 0), R);
+            }
+            if (__any_sync(0xffffffffu, b < a || a < top)) {
+                // out of order: an entry below an earlier one counts as that one
+                a = max(a, top);
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int o = __shfl_up_sync(0xffffffffu, a, d);
+                    if (lane >= d) a = max(a, o);
+                }
+                b = max(a, b);
             }
             const long long mine = static_cast<long long>((b - a + TT - 1) / TT) * NT;
             long long sum = mine;
@@ -110,6 +121,7 @@ struct TileWalk {
                 return true;
             }
             before += __shfl_sync(0xffffffffu, sum, 31);
+            top = __shfl_sync(0xffffffffu, b, 31);
             base += 32;
         }
         return false;

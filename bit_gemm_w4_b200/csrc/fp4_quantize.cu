@@ -80,13 +80,18 @@ __global__ void __launch_bounds__(512) fp4_quantize_kernel(QuantArgs a) {
     if constexpr (kOrdered) {
         long long slot = r / a.order.HT, x = r % a.order.HT;
         if (a.order.offsets && real) {
-            // the last matrix that begins at or before the row
-            int e = -1;
-            for (int i = tx & 31; i - (tx & 31) < a.order.E; i += 32) {
-                const bool before = i < a.order.E && min(max(load_i32(a.order.offsets + i), 0), static_cast<int>(a.rows)) <= r;
-                e += __popc(__ballot_sync(0xffffffffu, before));
+            // the last matrix that begins at or before the row; an entry below
+            // an earlier one counts as that one
+            int e = -1, first = 0;
+            for (int base = 0; base < a.order.E; base += 32) {
+                const int i = base + (tx & 31);
+                const int at = i < a.order.E ? min(max(load_i32(a.order.offsets + i), 0), static_cast<int>(a.rows)) : 0;
+                const uint32_t after = __ballot_sync(0xffffffffu, i >= a.order.E || at > r);
+                const int n = after ? __ffs(after) - 1 : 32;
+                e += n;
+                first = max(first, __reduce_max_sync(0xffffffffu, (tx & 31) < n ? at : 0));
+                if (n < 32) break;
             }
-            const int first = e < 0 ? 0 : min(max(load_i32(a.order.offsets + e), 0), static_cast<int>(a.rows));
             slot = e < 0 ? -1 : first / a.order.HT + e + (r - first) / a.order.HT;
             x = (r - first) % a.order.HT;
         }

@@ -479,8 +479,8 @@ mq_status mq_fp4_linear_codes(const mq_fp4_weight *w, const void *codes, const v
 
 /* The products of a mixture of experts: R rows grouped by matrix, Y[r] =
  * x[r] W[e]^T for offsets[e] <= r < offsets[e + 1] (offsets: int32 [E + 1],
- * device, ascending within [0, R]; out-of-range or descending entries are
- * clamped to that, never followed outside the buffers). x[r] is X row
+ * device, ascending within [0, R]; entries out of range are clamped to it,
+ * and an entry below an earlier one counts as that one). x[r] is X row
  * index[r], or X row r when index is NULL, as in mq_fp4_quantize. Rows of Y
  * outside [offsets[0], offsets[E]) are left as they were. Workspace for R
  * rows. The device reads the offsets; the host does not wait for them.

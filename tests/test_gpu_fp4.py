@@ -347,6 +347,29 @@ def test_grouped_bad_offsets_stay_inside(mq, cuda, fmt, offsets):
     assert w.device_error() == 0
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R", [9, 60, 900])
+@pytest.mark.parametrize("E", [4, 70])
+def test_grouped_descending_offsets(mq, cuda, fmt, R, E):
+    # an entry below an earlier one counts as that one: no row belongs to two matrices
+    N, K = 96, 300
+    w = mq.Fp4Weight.pack(values(E * N, K, BF16, 1).view(E, N, K).to(cuda), fmt)
+    X = values(R, K, BF16, 2).to(cuda)
+    g = torch.Generator().manual_seed(R + E)
+    offsets = torch.randint(-R // 4, R + R // 4, (E + 1,), generator=g).sort().values
+    swap = torch.randint(0, E + 1, (E // 2,), generator=g)
+    offsets[swap] = offsets[swap.flip(0)]
+    offsets[0] = 0
+    ascending = offsets.clamp(0, R).cummax(0).values
+    want = torch.full((R, N), 3.0, dtype=BF16, device=cuda)
+    w.linear_grouped(X, ascending.int().to(cuda), want)
+    for x in (X, mq.fp4_quantize(X, fmt)):
+        Y = torch.full_like(want, 3.0)
+        w.linear_grouped(x, offsets.int().to(cuda), Y)
+        assert torch.equal(Y, want)
+    assert w.device_error() == 0
+
+
 # ---------------------------------------------------------------- refusals on the device's side
 def test_refusals(mq, cuda):
     w1 = mq.Fp4Weight.pack(values(64, 64, BF16, 1).to(cuda), "nvfp4")
