@@ -144,20 +144,32 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// v[j] * f[j] * w for sixteen tokens, each product rounded; f: 16 bytes aligned.
+// v * f * w with a token's and a weight row's factor (at least 2^-100), two
+// roundings: by the weight's first where that is at most 1, else last, so that
+// nothing between overflows or underflows that the result does not.
+__device__ __forceinline__ float apply_factor(float v, float f, float w) {
+    return w <= 1.0f ? v * w * f : v * f * w;
+}
+
+// apply_factor for sixteen tokens; f: 16 bytes aligned.
 __device__ __forceinline__ void apply_factors(float (&v)[16], const float *f, float w) {
-    const uint64_t w2 = pack2(w, w);
+    const bool small = w <= 1.0f;
+    const uint64_t w2 = pack2(small ? w : 1.0f, small ? w : 1.0f);
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
         const ulonglong2 g = *reinterpret_cast<const ulonglong2 *>(f + j);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
             uint64_t d;
-            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(v[j + i], v[j + i + 1])), "l"(i ? g.y : g.x));
-            asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(w2));
+            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pack2(v[j + i], v[j + i + 1])), "l"(w2));
+            asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(i ? g.y : g.x));
             v[j + i] = __uint_as_float(static_cast<uint32_t>(d));
             v[j + i + 1] = __uint_as_float(static_cast<uint32_t>(d >> 32));
         }
+    }
+    if (!small) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= w;
     }
 }
 

@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_co
                 float y = part[0];
 #pragma unroll
                 for (int r = 1; r < 8; ++r) y += part[r];  // those past `split` are zeros
-                if constexpr (NV) y = y * factors[m] * wfactors[first + w];
+                if constexpr (NV) y = apply_factor(y, factors[m], wfactors[first + w]);
                 if (n < p.N) store_output(p.Y, (m0 + m) * p.ldy + n, y, p.fp16);
             }
         }

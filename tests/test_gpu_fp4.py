@@ -217,6 +217,28 @@ def test_linear_strides_and_canaries(mq, cuda, fmt, M):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(5, 300, 512), (6, 200, 2048), (50, 200, 1792), (300, 260, 512)])
+def test_linear_largest_and_smallest(mq, cuda, fmt, M, N, K):
+    # whatever the rows' sizes, an output is finite and right where it and the
+    # sums on the way to it are
+    X, W = values(M, K, FP32, M, spread=0.3), values(N, K, FP32, N, spread=0.3)
+    X = (X * torch.tensor([1e35, 1e-25, 1.0, 1e20, 1e-12])[torch.arange(M) % 5][:, None]).to(BF16)
+    W = W * torch.tensor([1e-25, 1e34, 1e-3, 1e10, 1e-12, 1e18, 1.0])[torch.arange(N) % 7][:, None]
+    w = mq.Fp4Weight.pack(W.to(cuda), fmt)
+    x64, w64 = held(X, fmt), held(W, fmt)
+    y64, S = fp4.linear(x64, w64)
+    got = w.linear(X.to(cuda)).double().cpu().numpy()
+    ok = S < 2.0**126
+    # as `bound`, but no fp16: bf16 and fp32 are normal down to 2^-126, where an
+    # fp32 step is 2^-149; the smallest S here are 2^-150 or so
+    tol = ((torch.finfo(BF16).eps / 2 + 2**-22) * np.abs(y64) + (K / 16 + 16) * 2.0**-23 * S * 1.01 +
+           (K / 16 + 16) * 2.0**-126)
+    assert np.isfinite(got[ok]).all() and (np.abs(got - y64)[ok] <= tol[ok]).all()
+    assert 0.7 < ok.mean() < 1
+    assert w.device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [5, 200])
 def test_linear_non_finite_rows(mq, cuda, fmt, M):
     N, K = 150, 400
