@@ -115,9 +115,11 @@ struct Raw {
     }
 };
 
+// Plain loads, not the read-only ones: a launch that started before the one
+// that writes X was over may not take X for read-only.
 __device__ __forceinline__ uint4 ldg128(const char *p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -155,7 +157,7 @@ __device__ __forceinline__ void load_chunk(Raw<T> &r, const RowSource &a, const 
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     uint4 v;
-                    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                  : "l"(q + 16 * i));
                     t[4 * i] = v.x;
@@ -184,10 +186,10 @@ __device__ __forceinline__ void load_chunk(Raw<T> &r, const RowSource &a, const 
     for (int i = 0; i < kChunk; ++i) {
         if (c + i >= a.K) break;
         if constexpr (sizeof(T) == 4) {
-            asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r.w[i]) : "l"(row + c + i));
+            asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.w[i]) : "l"(row + c + i));
         } else {
             unsigned short h;
-            asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(h) : "l"(row + c + i));
+            asm volatile("ld.global.b16 %0, [%1];" : "=h"(h) : "l"(row + c + i));
             r.w[i >> 1] |= static_cast<uint32_t>(h) << (16 * (i & 1));
         }
     }
@@ -198,7 +200,7 @@ template <class T>
 __device__ __forceinline__ void load_whole_chunk(Raw<T> &r, const T *p) {
 #pragma unroll
     for (int i = 0; i < Raw<T>::kWords / 8; ++i)
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(r.w[8 * i]), "=r"(r.w[8 * i + 1]), "=r"(r.w[8 * i + 2]), "=r"(r.w[8 * i + 3]),
                        "=r"(r.w[8 * i + 4]), "=r"(r.w[8 * i + 5]), "=r"(r.w[8 * i + 6]), "=r"(r.w[8 * i + 7])
                      : "l"(p + i * (32 / sizeof(T))));

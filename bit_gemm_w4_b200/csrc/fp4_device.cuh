@@ -34,12 +34,12 @@ __device__ __forceinline__ float load_f32(const float *p) {
 
 __device__ __forceinline__ uint32_t load_word(const uint32_t *p) {
     uint32_t v;
-    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint32_t load_byte(const uint8_t *p) {
     uint32_t v;
-    asm volatile("{\n\t.reg .u8 b;\n\tld.global.nc.u8 b, [%1];\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(v) : "l"(p));
+    asm volatile("{\n\t.reg .u8 b;\n\tld.global.u8 b, [%1];\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint4 load_u128(const void *p) {
