@@ -5,7 +5,6 @@
 
 #include <new>
 #include <string>
-#include <vector>
 
 #include "fp4.h"
 #include "kernels.h"
@@ -14,7 +13,8 @@ struct mq_fp4_weight {
     int device = -1;
     mq::Fp4Device d;
     int64_t device_bytes = 0;
-    std::vector<void *> allocations;
+    void *allocations[3];  // the first `allocated` of them
+    int allocated = 0;
 };
 
 namespace mq {
@@ -26,6 +26,7 @@ constexpr int64_t kMaxK = int64_t(1) << 24;
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 mq_status cuda_fail(cudaError_t e, const char *what) {
+    cudaGetLastError();  // reported here: whoever checks for the last error next has none of it
     return fail(e == cudaErrorMemoryAllocation ? MQ_ERR_OUT_OF_MEMORY : MQ_ERR_CUDA,
                 std::string(what) + ": " + cudaGetErrorString(e));
 }
@@ -90,7 +91,7 @@ mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
     auto get = [&](void **p, int64_t bytes) {
         const cudaError_t e = cudaMalloc(p, static_cast<size_t>(bytes));
         if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc");
-        w->allocations.push_back(*p);
+        w->allocations[w->allocated++] = *p;
         w->device_bytes += bytes;
         return MQ_OK;
     };
@@ -238,7 +239,7 @@ void mq_fp4_free(mq_fp4_weight *w) {
     bool switched = false;
     if (w->device >= 0 && cudaGetDevice(&prev) == cudaSuccess && prev != w->device)
         switched = cudaSetDevice(w->device) == cudaSuccess;
-    for (void *p : w->allocations) cudaFree(p);
+    for (int i = 0; i < w->allocated; ++i) cudaFree(w->allocations[i]);
     if (switched) cudaSetDevice(prev);
     delete w;
 }

@@ -428,10 +428,14 @@ mq_status launch_fp4_order(const Fp4Device &d, uint8_t *codes, uint8_t *scales, 
     const int units = fp4_stage_scales(d.fmt) / 4;
     const long long total = d.E * d.NT * d.KS * 1024;
     const long long blocks = std::min<long long>((total + 255) / 256, 32ll * sm_count());
-    fp4_order_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        d.pieces, codes, scales, total, d.N, d.NT, d.KS, units, fp4_code_pitch(d.K), fp4_scale_pitch(d.fmt, d.K),
-        to_rows);
-    const cudaError_t e = cudaPeekAtLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_order_kernel, d.pieces, codes, scales, total,
+                                             static_cast<long long>(d.N), static_cast<long long>(d.NT), d.KS, units,
+                                             static_cast<long long>(fp4_code_pitch(d.K)),
+                                             static_cast<long long>(fp4_scale_pitch(d.fmt, d.K)), to_rows);
     if (e != cudaSuccess)
         return fail(MQ_ERR_CUDA, std::string("fp4 order launch: ") + cudaGetErrorString(e));
     return MQ_OK;

@@ -279,6 +279,21 @@ def test_pack_and_export(mq, cuda, fmt):
     assert fmt == "mxfp4" or torch.equal(again.row_scale, e.row_scale)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_pack_too_large_for_the_device(mq, cuda, fmt):
+    # refused before anything is read; no error is left behind for the next launch to find
+    buf = torch.zeros(1024, dtype=torch.uint8, device=cuda)
+    h = mq.ctypes.c_void_p()
+    at, s = buf.data_ptr(), torch.cuda.current_stream().cuda_stream
+    lib, f = mq.lib(), mq.FP4_FORMATS[fmt]
+    assert lib.mq_fp4_pack_codes(at, at, at, 1, 1 << 30, 1 << 24, f, s, mq.ctypes.byref(h)) == mq.OUT_OF_MEMORY
+    assert lib.mq_fp4_pack(at, 0, 1, 1 << 30, 1 << 24, f, s, mq.ctypes.byref(h)) == mq.OUT_OF_MEMORY
+    assert not h.value
+    assert (buf + 1).sum().item() == 1024
+    W = values(40, 64, BF16, 1)
+    same_bits(mq.Fp4Weight.pack(W.to(cuda), fmt).export(), W, fmt)
+
+
 # ---------------------------------------------------------------- grouped
 def grouped_check(mq, cuda, fmt, dtype, N, K, counts, lead=0, tail=0, index=None, x_rows=None, seed=0):
     E, R = len(counts), lead + sum(counts) + tail
