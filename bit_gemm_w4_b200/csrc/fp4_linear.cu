@@ -4,7 +4,7 @@
 //   Y[r][n] = fx[r] * fw[n] * sum_k (cx[r][k] sx[r][k / B]) (cw[n][k] sw[n][k / B])
 //
 // The weight is the MMA's A operand (128 rows a tile), the tokens its B
-// operand (16 to 64 columns), so that a single token fills a tile of the
+// operand (16 to 128 columns), so that a single token fills a tile of the
 // tensor core; block scales are applied inside the MMA and the 32-bit row
 // factors (MQ_FP4_NV) when Y is stored. One CTA computes one tile over a share
 // of K; the CTAs of a cluster share a tile, push their partial sums into the
@@ -34,7 +34,7 @@ constexpr int kThreads = 320;
 constexpr int kFeeders = 256;  // threads of warps 2 to 9
 constexpr int kMaxStages = 8;
 constexpr int kBoxRows = 16;   // tokens of one copy
-constexpr int kMaxTT = 64;
+constexpr int kMaxTT = 128;  // what a scale unit holds
 
 struct NarrowParams {
     CUtensorMap tx;
@@ -53,7 +53,7 @@ struct NarrowParams {
     int *err;
     long long N;
     int NT, KS, E, R;
-    int TT;      // tokens of a tile: 16, 32 or 64
+    int TT;      // tokens of a tile, a multiple of 16
     int split;   // CTAs that share a tile (the cluster)
     int stages;  // ring slots
     int fp16;    // Y's type
@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_co
             const int row = threadIdx.x - 64;
             wfactors[row] = n0 + row < p.N ? __ldg(p.wfactor + static_cast<long long>(t.e) * p.N + n0 + row) : 0.0f;
         }
-    constexpr uint32_t tmem_cols = 128;
+    // the accumulator and both operands' scales; two CTAs of an SM share 512
+    const uint32_t tmem_cols = TT + 8 * kUnits <= 128 ? 128 : 256;
     if (warp == 1) tc5::alloc<1>(tmem_slot, tmem_cols);
     tc5::fence_before();
     __syncthreads();
@@ -504,19 +505,34 @@ struct Choice {
 Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
     const int64_t mats = grouped ? std::min<int64_t>(d.E, rows) : 1, per = (rows + mats - 1) / mats;
     const int64_t sms = d.sms;
-    // Up to 32 tokens: narrow, as long as its tiles run in one wave of two CTAs
-    // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
-    // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 64: narrow
-    // where K can be split between CTAs, which the wide form does not do (64 x
-    // 4096 x 11008: 14.4 us, wide 20.1; 64 x 11008 x 4096: 12.1 us, wide 11.6).
-    const int TT = per <= 16 ? 16 : per <= 32 ? 32 : 64;
     const int64_t likely = mats * d.NT;
-    const bool narrow = per <= 32 ? likely <= 2 * sms : per <= 64 && likely <= sms / 2;
     // K is split as far as that gives every SM at most one CTA: past it the
     // further CTAs start after the first ones' loads (1 x 4096 x 4096 takes
     // 9.1, 8.0, 8.5 and 9.3 us with 2, 4, 6 and 8; 1 x 11008 x 4096, 86 tiles,
-    // 11.8 us with 1 and 14.0 us with 4).
-    const int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sms / likely})));
+    // 11.8 us with 1 and 14.0 us with 4). A CTA of more than 32 tokens has its
+    // SM to itself, and the SMs' groups then hold only so many clusters at
+    // once (48 x 2048 x 2048, 16 tiles: 11.7 us with 8, 7.3 us with 4).
+    int split;
+    if (per <= 32) {
+        split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sms / likely})));
+    } else {
+        constexpr int kClusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};  // of 1 to 8 CTAs
+        split = static_cast<int>(std::min<int64_t>(8, d.KS));
+        while (split > 1 && likely > kClusters[split]) --split;
+    }
+    // Up to 32 tokens: narrow, as long as its tiles run in one wave of two CTAs
+    // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
+    // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 128: where
+    // splitting K, which the wide form does not do, takes enough stages off a
+    // CTA to pay for the sum, whose time goes with the tokens. nvfp4, narrow
+    // and wide: 80 x 4096 x 11008 (43 stages, 11 a CTA) 14.1 and 19.6 us, 128
+    // tokens 16.4 and 20.9; 80 x 1024 x 4096 (16, 2) 8.3 and 9.5, 128 tokens
+    // 9.9 and 10.0; 48 x 4096 x 4096 (16, 4) 9.0 and 9.8, 80 tokens 10.6 and
+    // 10.3. More than one tile of tokens gains nothing (192 x 4096 x 11008
+    // 20.7 and 21.3).
+    const int64_t saved = d.KS - (d.KS + split - 1) / split;
+    const bool narrow = per <= 32 ? likely <= 2 * sms : per <= kMaxTT && 6 * saved >= per;
+    const int TT = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : static_cast<int>((per + 15) / 16 * 16);
     return {narrow ? TT : 0, split, likely, per};
 }
 

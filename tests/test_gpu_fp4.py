@@ -153,7 +153,8 @@ def test_dequantize_types_and_strides(mq, cuda, fmt, dtype, M, K):
 LINEAR = [(1, 1, 1), (1, 128, 256), (1, 4096, 512), (2, 130, 64), (16, 128, 2048), (17, 300, 1001), (7, 1111, 32),
           (33, 257, 4100), (64, 640, 768), (65, 127, 300), (128, 128, 256), (129, 384, 1280), (250, 260, 515),
           (513, 200, 96), (1025, 512, 512), (3, 300, 1536), (5, 260, 1792), (40, 200, 1280), (50, 256, 1792),
-          (12, 512, 700), (16, 384, 5000)]
+          (12, 512, 700), (16, 384, 5000), (80, 200, 11008), (81, 1100, 4200), (100, 130, 5003), (113, 140, 11111),
+          (128, 390, 6144), (65, 700, 9000)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -331,6 +332,8 @@ def grouped_check(mq, cuda, fmt, dtype, N, K, counts, lead=0, tail=0, index=None
     (96, 768, [1] * 40, 0, 0),
     (384, 640, [64, 250, 7], 0, 0),
     (130, 260, [0] * 70 + [2, 0, 150] + [1] * 30, 4, 4),
+    (256, 11008, [150, 30], 3, 1),
+    (130, 8200, [0, 270, 20], 0, 5),
 ])
 def test_grouped(mq, cuda, fmt, dtype, N, K, counts, lead, tail):
     grouped_check(mq, cuda, fmt, dtype, N, K, counts, lead, tail, seed=N)
