@@ -258,6 +258,42 @@ def test_linear_non_finite_rows(mq, cuda, fmt, M):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(mq, cuda, fmt):
+    # 2^32 outputs, 2^31 inputs: the same rows again and again
+    rows, times, N, K = 4099, 16384, 64, 32
+    X, W = values(rows, K, BF16, 1, spread=0.3), values(N, K, BF16, 2, spread=0.3)
+    w = mq.Fp4Weight.pack(W.to(cuda), fmt)
+    big = X.to(cuda).repeat(times, 1)
+    Y = w.linear(big)
+    check_product(Y[:rows], held(X, fmt), held(W, fmt), BF16)
+    assert (Y.view(times, rows, N) == Y[:rows]).all()
+    del Y
+    q = mq.fp4_quantize(big, fmt)
+    same_bits(mq.Fp4Tensor(*(None if t is None else t[-rows:] for t in (q.codes, q.scales, q.row_scale)), K, fmt), X, fmt)
+    v = q.dequantize(BF16)
+    assert (v.view(times, rows, K) == v[:rows]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [2, 70])
+def test_longest_rows(mq, cuda, fmt, M):
+    # K = 2^24: every stage's place, with few values that are not zero and sums that are exact
+    K, N = 1 << 24, 3
+    X, W = torch.zeros(M, K, dtype=BF16, device=cuda), torch.zeros(N, K, dtype=BF16, device=cuda)
+    at = torch.arange(0, K, 65521, device=cuda)
+    X[:, at] = 1.0
+    X[:, -1] = 1.0
+    W[:, at] = (torch.arange(len(at), device=cuda) % 2 * 2 - 1).to(BF16)
+    W[1], W[2, -1] = 2 * W[0], 4.0
+    Y = mq.Fp4Weight.pack(W, fmt).linear(X)
+    x64, w64 = (held(t[:, torch.cat([at, at.new_tensor([K - 1])])], "mxfp4") for t in (X, W))
+    # both formats hold these values, nvfp4 but for the roundings of the row
+    # factors, and the sums of codes are exact; half a step of bf16 remains
+    want = x64 @ w64.T
+    assert (np.abs(Y.double().cpu().numpy() - want) <= (2.0**-8 + 2.0**-20) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_no_rows(mq, cuda, fmt):
     w = mq.Fp4Weight.pack(values(64, 64, BF16, 1).to(cuda), fmt)
     X = torch.empty(0, 64, dtype=BF16, device=cuda)
