@@ -524,12 +524,12 @@ Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
     // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
     // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 128: where
     // splitting K, which the wide form does not do, takes enough stages off a
-    // CTA to pay for the sum, whose time goes with the tokens. nvfp4, narrow
-    // and wide: 80 x 4096 x 11008 (43 stages, 11 a CTA) 14.1 and 19.6 us, 128
-    // tokens 16.4 and 20.9; 80 x 1024 x 4096 (16, 2) 8.3 and 9.5, 128 tokens
-    // 9.9 and 10.0; 48 x 4096 x 4096 (16, 4) 9.0 and 9.8, 80 tokens 10.6 and
-    // 10.3. More than one tile of tokens gains nothing (192 x 4096 x 11008
-    // 20.7 and 21.3).
+    // CTA to pay for the sum, whose time goes with the tokens. nvfp4 with its
+    // quantisation, narrow and wide: 80 x 4096 x 11008 (43 stages, 11 a CTA)
+    // 14.1 and 19.6 us, 128 tokens 16.4 and 20.9; 80 x 1024 x 4096 (16, 2) 8.3
+    // and 9.5, 128 tokens 9.9 and 10.0; 48 x 4096 x 4096 (16, 4) 9.0 and 9.8,
+    // 80 tokens 10.6 and 10.3. More than one tile of tokens gains nothing (192
+    // x 4096 x 11008 20.7 and 21.3).
     const int64_t saved = d.KS - (d.KS + split - 1) / split;
     const bool narrow = per <= 32 ? likely <= 2 * sms : per <= kMaxTT && 6 * saved >= per;
     const int TT = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : static_cast<int>((per + 15) / 16 * 16);
