@@ -572,6 +572,49 @@ def test_beside_the_other_linears(mq, cuda, fmt):
         return x
 
     assert torch.equal(run(torch.cuda.synchronize), run(lambda: None))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 9, 90, 300])
+def test_chain_in_a_graph(mq, cuda, fmt, M):
+    # launches that overlap, copies and fills between them, captured and
+    # replayed with other inputs: the same bits as call by call
+    D = 1024
+    ws = [mq.Fp4Weight.pack((values(D, D, BF16, k, spread=0.1) * 0.04).to(cuda), fmt) for k in range(3)]
+    experts = mq.Fp4Weight.pack((values(4 * D, D, BF16, 9, spread=0.1) * 0.04).view(4, D, D).to(cuda), fmt)
+    given = values(M, D, BF16, 7, spread=0.2).to(cuda)
+    cut = torch.tensor([0, M // 3, M // 3, M, M], dtype=torch.int32, device=cuda)
+    x, y, off = torch.empty_like(given), torch.empty_like(given), torch.empty_like(cut)
+
+    def step():
+        x.copy_(given)
+        off.copy_(cut)
+        for w in ws:
+            w.linear(x, y)
+            x.copy_(y)
+            y.zero_()
+        experts.linear_grouped(x, off, y)
+        off.zero_()
+        x.zero_()
+        q = mq.fp4_quantize(y, fmt)
+        y.zero_()
+        return ws[0].linear(q), q.dequantize(BF16)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for k in range(3):
+        given.copy_(values(M, D, BF16, 20 + k, spread=0.2))
+        cut.copy_(torch.tensor([0, M // 2, M, M, M] if k == 1 else [0, 0, M // 4, M // 2, M], dtype=torch.int32))
+        g.replay()
+        g.replay()
+        have = [t.clone() for t in got]
+        assert all(torch.equal(a, b) for a, b in zip(have, step()))
+    assert all(w.device_error() == 0 for w in ws + [experts])
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_other_stream(mq, cuda, fmt):
     w = mq.Fp4Weight.pack(values(300, 256, BF16, 1).to(cuda), fmt)
