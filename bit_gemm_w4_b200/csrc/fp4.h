@@ -11,6 +11,10 @@
 
 namespace mq {
 
+// What a CUDA call that failed is reported as. It clears the last error, which
+// other launches of this library look at and would take for their own.
+mq_status fp4_cuda_fail(cudaError_t e, const char *what);
+
 // One K stage of the products: 256 columns, 128 bytes of codes in a row (the
 // 128-byte swizzle's span), 16 (MQ_FP4_NV) or 8 (MQ_FP4_MX) scale bytes.
 constexpr int kFp4StageK = 256;

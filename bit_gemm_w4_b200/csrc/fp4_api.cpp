@@ -18,18 +18,19 @@ struct mq_fp4_weight {
 };
 
 namespace mq {
+
+mq_status fp4_cuda_fail(cudaError_t e, const char *what) {
+    cudaGetLastError();
+    return fail(e == cudaErrorMemoryAllocation ? MQ_ERR_OUT_OF_MEMORY : MQ_ERR_CUDA,
+                std::string(what) + ": " + cudaGetErrorString(e));
+}
+
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // rows, N, E * N
 constexpr int64_t kMaxK = int64_t(1) << 24;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-mq_status cuda_fail(cudaError_t e, const char *what) {
-    cudaGetLastError();  // reported here: whoever checks for the last error next has none of it
-    return fail(e == cudaErrorMemoryAllocation ? MQ_ERR_OUT_OF_MEMORY : MQ_ERR_CUDA,
-                std::string(what) + ": " + cudaGetErrorString(e));
-}
 
 mq_status check_format(int fmt) {
     return fmt == MQ_FP4_MX || fmt == MQ_FP4_NV ? MQ_OK : fail(MQ_ERR_INVALID_ARG, "unknown fp4 format");
@@ -90,7 +91,7 @@ mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
     d.NT = (N + 127) / 128;
     auto get = [&](void **p, int64_t bytes) {
         const cudaError_t e = cudaMalloc(p, static_cast<size_t>(bytes));
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+        if (e != cudaSuccess) return fp4_cuda_fail(e, "cudaMalloc");
         w->allocations[w->allocated++] = *p;
         w->device_bytes += bytes;
         return MQ_OK;
@@ -108,7 +109,7 @@ mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
 mq_status new_weight(mq_fp4_weight **out) {
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "no usable CUDA device");
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "no usable CUDA device");
     if (dev < 0 || dev >= 64) return fail(MQ_ERR_UNSUPPORTED, "device ordinal above 63");
     mq_fp4_weight *w = new (std::nothrow) mq_fp4_weight();
     if (!w) return fail(MQ_ERR_OUT_OF_MEMORY, "host allocation failed");
@@ -129,7 +130,7 @@ struct Workspace {
 
 mq_status check_device(const mq_fp4_weight *w) {
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return fail(MQ_ERR_CUDA, "cudaGetDevice failed");
+    if (const cudaError_t e = cudaGetDevice(&dev)) return fp4_cuda_fail(e, "no usable CUDA device");
     if (dev != w->device)
         return fail(MQ_ERR_INVALID_ARG, "the current device is not the device that packed the weight");
     return MQ_OK;
@@ -241,6 +242,7 @@ void mq_fp4_free(mq_fp4_weight *w) {
         switched = cudaSetDevice(w->device) == cudaSuccess;
     for (int i = 0; i < w->allocated; ++i) cudaFree(w->allocations[i]);
     if (switched) cudaSetDevice(prev);
+    cudaGetLastError();  // nothing is reported from here, nothing is left behind
     delete w;
 }
 
@@ -260,12 +262,12 @@ mq_status mq_fp4_pack_codes(const void *codes, const void *scales, const float *
         if (d.row_scale)
             e = cudaMemcpyAsync(d.row_scale, row_scale, E * N * 4, cudaMemcpyDeviceToDevice, s);
         if (e == cudaSuccess) e = cudaMemsetAsync(d.err, 0, 4, s);
-        if (e != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack_codes");
+        if (e != cudaSuccess) st = fp4_cuda_fail(e, "mq_fp4_pack_codes");
     }
     if (!st)
         st = launch_fp4_order(w->d, static_cast<uint8_t *>(const_cast<void *>(codes)),
                               static_cast<uint8_t *>(const_cast<void *>(scales)), false, s);
-    if (!st && (e = cudaStreamSynchronize(s)) != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack_codes");
+    if (!st && (e = cudaStreamSynchronize(s)) != cudaSuccess) st = fp4_cuda_fail(e, "mq_fp4_pack_codes");
     if (st) {
         mq_fp4_free(w);
         return st;
@@ -294,7 +296,7 @@ mq_status mq_fp4_pack(const void *W, mq_dtype dtype, int64_t E, int64_t N, int64
         e = cudaMalloc(reinterpret_cast<void **>(&rows),
                        static_cast<size_t>(code_bytes + E * N * fp4_scale_pitch(fmt, K)));
         if (e == cudaSuccess) e = cudaMemsetAsync(w->d.err, 0, 4, s);
-        if (e != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack");
+        if (e != cudaSuccess) st = fp4_cuda_fail(e, "mq_fp4_pack");
     }
     if (!st)
         st = launch_fp4_quantize(W, dtype, E * N, K, K, nullptr, E * N, fmt, rows, rows + code_bytes, w->d.row_scale,
@@ -302,8 +304,9 @@ mq_status mq_fp4_pack(const void *W, mq_dtype dtype, int64_t E, int64_t N, int64
     if (!st) st = launch_fp4_order(w->d, rows, rows + code_bytes, false, s);
     if (rows) {
         e = cudaStreamSynchronize(s);
-        if (!st && e != cudaSuccess) st = cuda_fail(e, "mq_fp4_pack");
+        if (!st && e != cudaSuccess) st = fp4_cuda_fail(e, "mq_fp4_pack");
         cudaFree(rows);
+        cudaGetLastError();
     }
     if (st) {
         mq_fp4_free(w);
@@ -334,7 +337,7 @@ mq_status mq_fp4_export(const mq_fp4_weight *w, void *codes, void *scales, float
     cudaError_t e = cudaMemsetAsync(scales, 0, d.E * d.N * fp4_scale_pitch(d.fmt, d.K), s);
     if (e == cudaSuccess && d.row_scale)
         e = cudaMemcpyAsync(row_scale, d.row_scale, d.E * d.N * 4, cudaMemcpyDeviceToDevice, s);
-    if (e != cudaSuccess) return cuda_fail(e, "mq_fp4_export");
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "mq_fp4_export");
     return launch_fp4_order(d, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), true, s);
 }
 
@@ -381,7 +384,7 @@ mq_status mq_fp4_device_error(const mq_fp4_weight *w, mq_stream stream, int32_t 
     int v = 0;
     if (e == cudaSuccess) e = cudaMemcpy(&v, w->d.err, 4, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && v) e = cudaMemset(w->d.err, 0, 4);
-    if (e != cudaSuccess) return cuda_fail(e, "mq_fp4_device_error");
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "mq_fp4_device_error");
     *code = v;
     return v ? fail(MQ_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait") : MQ_OK;
 }

@@ -464,9 +464,9 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
     p.paired = d.N % 2 == 0 && p.ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 3) == 0;
     static bool configured[64] = {};
     if (!configured[d.device]) {
-        if (cudaFuncSetAttribute(fp4_narrow_kernel<NV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-            cudaSuccess)
-            return fail(MQ_ERR_CUDA, "fp4 linear: device setup failed");
+        if (const cudaError_t e = cudaFuncSetAttribute(fp4_narrow_kernel<NV, T>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024))
+            return fp4_cuda_fail(e, "fp4 linear: device setup");
         configured[d.device] = true;
     }
     cudaLaunchConfig_t cfg = {};
@@ -489,7 +489,7 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
     cfg.attrs = attr;
     cfg.numAttrs = na;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_narrow_kernel<NV, T>, p);
-    if (e != cudaSuccess) return fail(MQ_ERR_CUDA, std::string("fp4 linear launch: ") + cudaGetErrorString(e));
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "fp4 linear launch");
     return MQ_OK;
 }
 

@@ -189,8 +189,7 @@ mq_status run_quantize(const QuantArgs &a, int bx, cudaStream_t stream) {
     if (!a.order.HT)
         e = launch_after(fp4_quantize_kernel<T, NV, kChunks, false>, a, dim3(static_cast<unsigned>(grid)), dim3(bx, by),
                          stream);
-    if (e != cudaSuccess)
-        return fail(MQ_ERR_CUDA, std::string("fp4 quantisation launch: ") + cudaGetErrorString(e));
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "fp4 quantisation launch");
     return MQ_OK;
 }
 
@@ -348,8 +347,7 @@ mq_status run_dequantize(const DequantArgs &a, cudaStream_t stream) {
     if (gx > 0x7FFFFFFFll || gy > 65535) return fail(MQ_ERR_UNSUPPORTED, "fp4 dequantisation: too large");
     const cudaError_t e = launch_after(fp4_dequantize_kernel<T, NV>, a,
                                        dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(bx, by), stream);
-    if (e != cudaSuccess)
-        return fail(MQ_ERR_CUDA, std::string("fp4 dequantisation launch: ") + cudaGetErrorString(e));
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "fp4 dequantisation launch");
     return MQ_OK;
 }
 
@@ -436,8 +434,7 @@ mq_status launch_fp4_order(const Fp4Device &d, uint8_t *codes, uint8_t *scales, 
                                              static_cast<long long>(d.N), static_cast<long long>(d.NT), d.KS, units,
                                              static_cast<long long>(fp4_code_pitch(d.K)),
                                              static_cast<long long>(fp4_scale_pitch(d.fmt, d.K)), to_rows);
-    if (e != cudaSuccess)
-        return fail(MQ_ERR_CUDA, std::string("fp4 order launch: ") + cudaGetErrorString(e));
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "fp4 order launch");
     return MQ_OK;
 }
 

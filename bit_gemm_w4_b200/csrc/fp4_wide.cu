@@ -432,9 +432,9 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     p.wait_first = offsets && !chained;
     static bool configured[64] = {};
     if (!configured[d.device]) {
-        if (cudaFuncSetAttribute(fp4_wide_kernel<NV, kHalves>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-            cudaSuccess)
-            return fail(MQ_ERR_CUDA, "fp4 linear: device setup failed");
+        if (const cudaError_t e = cudaFuncSetAttribute(fp4_wide_kernel<NV, kHalves>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024))
+            return fp4_cuda_fail(e, "fp4 linear: device setup");
         configured[d.device] = true;
     }
     cudaLaunchConfig_t cfg = {};
@@ -452,7 +452,7 @@ static mq_status run_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *o
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_wide_kernel<NV, kHalves>, p);
-    if (e != cudaSuccess) return fail(MQ_ERR_CUDA, std::string("fp4 linear launch: ") + cudaGetErrorString(e));
+    if (e != cudaSuccess) return fp4_cuda_fail(e, "fp4 linear launch");
     return MQ_OK;
 }
 
