@@ -274,6 +274,10 @@ def test_offsets_past_32_bits(mq, cuda, fmt):
     assert (v.view(times, rows, K) == v[:rows]).all()
 
 
+# the same name is defined once more below: this one is collected under its own
+test_more_than_2_32_outputs = test_offsets_past_32_bits
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [2, 70])
 def test_longest_rows(mq, cuda, fmt, M):
