@@ -120,9 +120,15 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_co
     if constexpr (kQuantise)
         if (threadIdx.x >= 64)
             for (int i = threadIdx.x - 64; i < TT; i += kFeeders) tops[i] = 0;
-    // Whatever follows on the stream may start: it waits for this launch
-    // before it reads anything but packed weights.
-    pdl_launch_dependents();
+    // Tensor memory for the accumulator and both operands' scales (two CTAs of
+    // an SM share 512 columns). Only with it in hand may whatever follows on the
+    // stream start: that waits for this launch before it reads anything but
+    // packed weights, and may take the rest of the tensor memory before.
+    const uint32_t tmem_cols = TT + 8 * kUnits <= 128 ? 128 : 256;
+    if (warp == 1) {
+        tc5::alloc<1>(tmem_slot, tmem_cols);
+        pdl_launch_dependents();
+    }
     if (p.wait_first) pdl_wait();  // the offsets may come from the launch just before
     Tile t{0, 0, 0, 0, 0};
     TileWalk walk(p.offsets, p.E, p.R, TT, p.NT);
@@ -150,9 +156,6 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_co
             const int row = threadIdx.x - 64;
             wfactors[row] = n0 + row < p.N ? __ldg(p.wfactor + static_cast<long long>(t.e) * p.N + n0 + row) : 0.0f;
         }
-    // the accumulator and both operands' scales; two CTAs of an SM share 512
-    const uint32_t tmem_cols = TT + 8 * kUnits <= 128 ? 128 : 256;
-    if (warp == 1) tc5::alloc<1>(tmem_slot, tmem_cols);
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
