@@ -116,12 +116,25 @@ mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype d
 // are quantised for it.
 Fp4Order fp4_token_order(const Fp4Device &d, int64_t rows, const int32_t *offsets);
 
+// Bytes that the scales of up to `rows` rows quantised for launch_fp4_linear
+// take at most, in whichever order: no less for more rows.
+int64_t fp4_token_scale_bytes(const Fp4Device &d, int64_t rows);
+
 // The form of launch_fp4_linear for many tokens (fp4_wide.cu): the tokens of
 // a tile and the halves they come in.
 struct Fp4WidePlan {
     int TT, halves;
 };
 Fp4WidePlan fp4_wide_plan(const Fp4Device &d, int64_t rows);
+// Its tiles, the smallest first, and whether up to `rows` rows may take tile i:
+// not where every smaller count of rows fits as many of the tiles before it,
+// which take less time each.
+constexpr int kFp4WideTiles[] = {32, 64, 96, 128, 160, 192, 224, 256, 320, 384};
+inline int fp4_wide_halves(int TT) { return TT > 224 ? 2 : 1; }
+inline int fp4_scale_unit(int HT) { return HT > 128 ? 1024 : 512; }
+inline bool fp4_wide_may_take(const Fp4Device &d, int64_t rows, int i) {
+    return i == 0 || rows > (d.E == 1 ? kFp4WideTiles[i - 1] : d.E * kFp4WideTiles[i - 1] / 2);
+}
 mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                           mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
 

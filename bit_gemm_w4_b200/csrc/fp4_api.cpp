@@ -118,13 +118,14 @@ mq_status new_weight(mq_fp4_weight **out) {
     return MQ_OK;
 }
 
-// The buffers of R quantised rows inside a workspace.
+// The buffers of R quantised rows inside a workspace, whose size grows with R:
+// one for a program's largest batch serves the smaller ones.
 struct Workspace {
-    int64_t scales, factors, total;
-    Workspace(int64_t R, int64_t K, int fmt, const Fp4Order &order) {
-        scales = R * fp4_code_pitch(K);
-        factors = scales + (order.HT ? order.bytes(fmt) : R * fp4_scale_pitch(fmt, K));
-        total = factors + (fmt == MQ_FP4_NV ? (R * 4 + 15) / 16 * 16 : 0);
+    int64_t factors, scales, total;
+    Workspace(const Fp4Device &d, int64_t R) {
+        factors = R * fp4_code_pitch(d.K);
+        scales = factors + (d.fmt == MQ_FP4_NV ? (R * 4 + 127) / 128 * 128 : 0);
+        total = scales + fp4_token_scale_bytes(d, R);
     }
 };
 
@@ -158,7 +159,7 @@ mq_status quantize_and_multiply(const mq_fp4_weight *w, const void *X, int dtype
         return launch_fp4_linear_direct(d, X, static_cast<mq_dtype>(dtype), R, ldx, index, x_rows, offsets, Y, ldy, s);
     }
     const Fp4Order order = fp4_token_order(d, R, offsets);
-    const Workspace ws(R, d.K, d.fmt, order);
+    const Workspace ws(d, R);
     if (!workspace || !aligned16(workspace)) return fail(MQ_ERR_INVALID_ARG, "the workspace is NULL or not 16-byte aligned");
     if (workspace_bytes < static_cast<size_t>(ws.total))
         return fail(MQ_ERR_INVALID_ARG, "workspace smaller than mq_fp4_workspace_bytes");
@@ -343,7 +344,7 @@ mq_status mq_fp4_export(const mq_fp4_weight *w, void *codes, void *scales, float
 
 int64_t mq_fp4_workspace_bytes(const mq_fp4_weight *w, int64_t rows) {
     if (!w || rows <= 0 || rows > kMaxRows || fp4_linear_quantises(w->d, rows)) return 0;
-    return Workspace(rows, w->d.K, w->d.fmt, fp4_token_order(w->d, rows, nullptr)).total;
+    return Workspace(w->d, rows).total;
 }
 
 mq_status mq_fp4_linear(const mq_fp4_weight *w, const void *X, mq_dtype dtype, int64_t M, int64_t ldx, void *Y,

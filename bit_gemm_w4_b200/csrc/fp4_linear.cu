@@ -564,19 +564,40 @@ mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t 
 // place: 2048 x 14336 x 4096 nvfp4, at the power limit, takes 76 us instead of
 // 92 us (with the quantisation). Not for many matrices with few rows each,
 // whose slots would be mostly empty.
-Fp4Order fp4_token_order(const Fp4Device &d, int64_t rows, const int32_t *offsets) {
+static bool ordered(const Fp4Device &d, int64_t rows, int HT) { return d.E <= 8 * (rows / HT) + 256; }
+
+static Fp4Order token_order(const Fp4Device &d, int64_t rows, int HT) {
     Fp4Order o;
-    if (choose(d, rows, d.E > 1).TT) return o;
-    const Fp4WidePlan plan = fp4_wide_plan(d, rows);
-    const int HT = plan.TT / plan.halves;
-    if (d.E > 8 * (rows / HT) + 256) return o;
     o.HT = HT;
-    o.unit = HT > 128 ? 1024 : 512;
+    o.unit = fp4_scale_unit(HT);
     o.KS = d.KS;
     o.slots = rows / HT + d.E + 1;
-    o.offsets = offsets;
     o.E = static_cast<int>(d.E);
     return o;
+}
+
+Fp4Order fp4_token_order(const Fp4Device &d, int64_t rows, const int32_t *offsets) {
+    if (choose(d, rows, d.E > 1).TT) return {};
+    const Fp4WidePlan plan = fp4_wide_plan(d, rows);
+    const int HT = plan.TT / plan.halves;
+    if (!ordered(d, rows, HT)) return {};
+    Fp4Order o = token_order(d, rows, HT);
+    o.offsets = offsets;
+    return o;
+}
+
+int64_t fp4_token_scale_bytes(const Fp4Device &d, int64_t rows) {
+    int64_t most = rows * fp4_scale_pitch(d.fmt, d.K);
+    // narrow tiles of up to 32 tokens: fewer rows take them too
+    const Choice c = choose(d, rows, d.E > 1);
+    if (c.TT && c.per <= 32) return most;
+    int i = 0;
+    for (int TT : kFp4WideTiles) {
+        if (!fp4_wide_may_take(d, rows, i++)) break;
+        const int HT = TT / fp4_wide_halves(TT);
+        if (ordered(d, rows, HT)) most = std::max(most, token_order(d, rows, HT).bytes(d.fmt));
+    }
+    return most;
 }
 
 // Whether the product quantises its tokens itself: the launch and the round

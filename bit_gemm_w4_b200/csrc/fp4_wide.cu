@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <iterator>
 
 #include "common.cuh"
 #include "fp4.h"
@@ -469,8 +470,9 @@ Fp4WidePlan fp4_wide_plan(const Fp4Device &d, int64_t rows) {
     const int64_t NT = (d.NT + 1) / 2, pairs = d.sms / 2, mats = std::min<int64_t>(d.E, rows);
     int best = 0;
     double least = 0;
-    for (int TT : {384, 320, 256, 224, 192, 160, 128, 96, 64, 32}) {
-        const bool two = TT > 224;
+    for (int i = std::size(kFp4WideTiles); i-- > 0;) {
+        const int TT = kFp4WideTiles[i];
+        const bool two = fp4_wide_halves(TT) == 2;
         const double even = static_cast<double>((rows + mats * TT - 1) / (mats * TT)) * mats;
         const double tiles = (mats == 1 ? even : std::max<double>(mats, static_cast<double>(rows) / TT + 0.5 * mats)) * NT;
         double waves = tiles / pairs;
@@ -479,7 +481,7 @@ Fp4WidePlan fp4_wide_plan(const Fp4Device &d, int64_t rows) {
         const double cost = waves * (d.KS * stage + (two ? 1000 : 0));
         if (!best || cost < least) least = cost, best = TT;
     }
-    return {best, best > 224 ? 2 : 1};
+    return {best, fp4_wide_halves(best)};
 }
 
 mq_status launch_fp4_wide(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y, mq_dtype dtype,

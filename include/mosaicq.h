@@ -453,8 +453,9 @@ mq_status mq_fp4_get_info(const mq_fp4_weight *w, mq_fp4_info *out);
 mq_status mq_fp4_export(const mq_fp4_weight *w, void *codes, void *scales, float *row_scale,
                         mq_stream stream);
 
-/* Device bytes the products below need to quantise `rows` rows: 0 where they
- * do so on the way (few rows), and then the workspace may be NULL. */
+/* Device bytes the products below need to quantise up to `rows` rows (never
+ * less for more rows): 0 where they do so on the way (few rows), and then the
+ * workspace may be NULL. */
 int64_t mq_fp4_workspace_bytes(const mq_fp4_weight *w, int64_t rows);
 
 /* Y = X W^T for a handle of one matrix: X [M][K] (bf16 or fp16, stride ldx)

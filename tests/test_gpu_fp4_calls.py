@@ -43,3 +43,22 @@ def test_a_refused_launch_leaves_no_error_behind(mq, cuda, fmt, call):
     assert torch.equal(got, want)
     assert run() == 0  # the stream takes launches again
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("E,N,K", [(1, 200, 96), (1, 1024, 4096), (1, 11007, 4100), (8, 1000, 640), (40, 384, 512),
+                                   (300, 72, 192)])
+def test_a_workspace_for_the_largest_batch_serves_the_smaller_ones(mq, cuda, fmt, E, N, K):
+    w = mq.Fp4Weight.pack(values(E * N, K, BF16, 1).view(E, N, K).to(cuda), fmt)
+    need = [w.workspace_bytes(r) for r in range(1, 4001)]
+    assert need == sorted(need)
+    for most in (17, 65, 129, 225, 257, 385, 2369):
+        ws = torch.full((need[most - 1] + 64,), 9, dtype=torch.uint8, device=cuda)
+        for M in (most, most - 1, most // 2, 1):
+            X = values(M, K, BF16, M, spread=0.3).to(cuda)
+            offsets = torch.linspace(0, M, E + 1).int().to(cuda)
+            Y = w.linear_grouped(X, offsets, None, ws[:-64])
+            assert torch.equal(Y, w.linear_grouped(mq.fp4_quantize(X, fmt), offsets))
+            assert E > 1 or torch.equal(Y, w.linear(X, None, ws[:-64]))
+        assert (ws[-64:] == 9).all()
+    assert w.device_error() == 0
