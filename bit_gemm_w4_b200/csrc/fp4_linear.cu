@@ -444,19 +444,79 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_narrow_kernel(const __grid_co
     }
 }
 
+// Ring slots of a CTA that shares its SM with `each` - 1 others.
+int narrow_stages(int fmt, int TT, int split, int each) {
+    const int room = (each == 2 ? 113 : 227) * 1024;
+    return std::min(kMaxStages, fmt == MQ_FP4_NV
+                                    ? (room - NarrowSmem<true>::fixed(TT, split)) / NarrowSmem<true>::slot(TT)
+                                    : (room - NarrowSmem<false>::fixed(TT, split)) / NarrowSmem<false>::slot(TT));
+}
+
+// How a product is run, from its sizes alone (the rows of each matrix are not
+// known to the host: `per` is their average).
+struct Choice {
+    int TT;          // tokens of a narrow tile; 0: the wide form
+    int split;       // CTAs that share a narrow tile
+    int each;        // narrow CTAs that share an SM
+    int64_t likely;  // narrow tiles of the matrices that have rows
+    int64_t per;     // rows of a matrix that has some
+};
+
+Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
+    const int64_t mats = grouped ? std::min<int64_t>(d.E, rows) : 1, per = (rows + mats - 1) / mats;
+    const int64_t sms = d.sms;
+    const int64_t likely = mats * d.NT;
+    const int TT = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : static_cast<int>((per + 15) / 16 * 16);
+    // K is split as far as that gives every SM at most one CTA: past it the
+    // further CTAs start after the first ones' loads (1 x 4096 x 4096 takes
+    // 9.1, 8.0, 8.5 and 9.3 us with 2, 4, 6 and 8; 1 x 11008 x 4096, 86 tiles,
+    // 11.8 us with 1 and 14.0 us with 4).
+    int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sms / likely})));
+    // CTAs of up to 16 tokens share an SM, so that the next launch's may start
+    // beside them. More tokens leave a CTA its SM, and a ring of up to eight
+    // slots, as long as all clusters run at once that way: the SMs' groups hold
+    // only so many, and the others wait for the first to end (nvfp4 24 x 2048 x
+    // 2048, 16 tiles: 9.4 us with 8 CTAs a cluster, 6.3 us with 6). Where they do
+    // not, up to 32 tokens two share an SM if each then has four slots, which
+    // nvfp4 with partial sums has not; else K is split less. One an SM and two,
+    // in us: nvfp4 24 x 11008 x 4096 (86 tiles) 10.2 and 11.8, 24 x 28672 x 8192
+    // (224) 32.2 and 25.9; mxfp4 24 x 11008 x 4096 8.9 and 10.4, 48 x 8192 x 8192
+    // 13.8 and 16.1.
+    int each = per <= 16 ? 2 : 1;
+    constexpr int kClusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};  // of 1 to 8 CTAs, one an SM
+    while (each == 1 && likely > kClusters[split]) {
+        if (per <= 32 && narrow_stages(d.fmt, TT, split, 2) >= 4)
+            each = 2;
+        else if (split > 1)
+            --split;
+        else
+            break;
+    }
+    // Up to 32 tokens: narrow, as long as its tiles run in one wave of two CTAs
+    // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
+    // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 128: where
+    // splitting K, which the wide form does not do, takes enough stages off a
+    // CTA to pay for the sum, whose time goes with the tokens. nvfp4 with its
+    // quantisation, narrow and wide: 80 x 4096 x 11008 (43 stages, 11 a CTA)
+    // 14.1 and 19.6 us, 128 tokens 16.4 and 20.9; 80 x 1024 x 4096 (16, 2) 8.3
+    // and 9.5, 128 tokens 9.9 and 10.0; 48 x 4096 x 4096 (16, 4) 9.0 and 9.8,
+    // 80 tokens 10.6 and 10.3. More than one tile of tokens gains nothing (192
+    // x 4096 x 11008 20.7 and 21.3).
+    const int64_t saved = d.KS - (d.KS + split - 1) / split;
+    const bool narrow = per <= 32 ? likely <= 2 * sms : per <= kMaxTT && 6 * saved >= per;
+    return {narrow ? TT : 0, split, each, likely, per};
+}
+
 template <bool NV, class T>
-mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, int split, bool chained,
+mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, const Choice &c, bool chained,
                      cudaStream_t stream) {
     using S = NarrowSmem<NV>;
-    p.TT = TT;
+    p.TT = c.TT;
     // the most tiles that any split of the rows into matrices makes
     const int64_t tiles = (p.offsets ? std::min<int64_t>(d.E, rows) + rows / p.TT : (rows + p.TT - 1) / p.TT) * d.NT;
-    p.split = split;
-    // Two CTAs an SM where each then has a ring of four stages, else one.
-    const int each = (113 * 1024 - S::fixed(p.TT, 8)) / S::slot(p.TT) >= 4 ? 2 : 1;
-    const int budget = each == 2 ? 113 * 1024 : 227 * 1024;
+    p.split = c.split;
     if (tiles * p.split > 0x7FFFFFFFll) return fail(MQ_ERR_UNSUPPORTED, "fp4 linear: too many tiles");
-    p.stages = std::min(kMaxStages, (budget - S::fixed(p.TT, p.split)) / S::slot(p.TT));
+    p.stages = narrow_stages(d.fmt, p.TT, p.split, c.each);
     const int smem = S::total(p.TT, p.split, p.stages);
     p.pieces = d.pieces;
     p.wfactor = d.row_scale;
@@ -499,49 +559,6 @@ mq_status run_narrow(const Fp4Device &d, NarrowParams &p, int64_t rows, int TT, 
     return MQ_OK;
 }
 
-// How a product is run, from its sizes alone (the rows of each matrix are not
-// known to the host: `per` is their average).
-struct Choice {
-    int TT;          // tokens of a narrow tile; 0: the wide form
-    int split;       // CTAs that share a narrow tile
-    int64_t likely;  // narrow tiles of the matrices that have rows
-    int64_t per;     // rows of a matrix that has some
-};
-
-Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
-    const int64_t mats = grouped ? std::min<int64_t>(d.E, rows) : 1, per = (rows + mats - 1) / mats;
-    const int64_t sms = d.sms;
-    const int64_t likely = mats * d.NT;
-    // K is split as far as that gives every SM at most one CTA: past it the
-    // further CTAs start after the first ones' loads (1 x 4096 x 4096 takes
-    // 9.1, 8.0, 8.5 and 9.3 us with 2, 4, 6 and 8; 1 x 11008 x 4096, 86 tiles,
-    // 11.8 us with 1 and 14.0 us with 4). A CTA of more than 32 tokens has its
-    // SM to itself, and the SMs' groups then hold only so many clusters at
-    // once (48 x 2048 x 2048, 16 tiles: 11.7 us with 8, 7.3 us with 4).
-    int split;
-    if (per <= 32) {
-        split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sms / likely})));
-    } else {
-        constexpr int kClusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};  // of 1 to 8 CTAs
-        split = static_cast<int>(std::min<int64_t>(8, d.KS));
-        while (split > 1 && likely > kClusters[split]) --split;
-    }
-    // Up to 32 tokens: narrow, as long as its tiles run in one wave of two CTAs
-    // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
-    // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 128: where
-    // splitting K, which the wide form does not do, takes enough stages off a
-    // CTA to pay for the sum, whose time goes with the tokens. nvfp4 with its
-    // quantisation, narrow and wide: 80 x 4096 x 11008 (43 stages, 11 a CTA)
-    // 14.1 and 19.6 us, 128 tokens 16.4 and 20.9; 80 x 1024 x 4096 (16, 2) 8.3
-    // and 9.5, 128 tokens 9.9 and 10.0; 48 x 4096 x 4096 (16, 4) 9.0 and 9.8,
-    // 80 tokens 10.6 and 10.3. More than one tile of tokens gains nothing (192
-    // x 4096 x 11008 20.7 and 21.3).
-    const int64_t saved = d.KS - (d.KS + split - 1) / split;
-    const bool narrow = per <= 32 ? likely <= 2 * sms : per <= kMaxTT && 6 * saved >= per;
-    const int TT = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : static_cast<int>((per + 15) / 16 * 16);
-    return {narrow ? TT : 0, split, likely, per};
-}
-
 }  // namespace
 
 mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
@@ -559,8 +576,8 @@ mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t 
     p.Y = Y;
     p.ldy = ldy;
     p.fp16 = dtype == MQ_FP16;
-    return d.fmt == MQ_FP4_NV ? run_narrow<true, void>(d, p, x.rows, c.TT, c.split, chained, stream)
-                              : run_narrow<false, void>(d, p, x.rows, c.TT, c.split, chained, stream);
+    return d.fmt == MQ_FP4_NV ? run_narrow<true, void>(d, p, x.rows, c, chained, stream)
+                              : run_narrow<false, void>(d, p, x.rows, c, chained, stream);
 }
 
 // Ordered for the wide form, whose four loader warps then have nothing to
@@ -635,10 +652,10 @@ mq_status launch_fp4_linear_direct(const Fp4Device &d, const void *X, mq_dtype d
     p.ldy = ldy;
     p.fp16 = dtype == MQ_FP16;
     if (dtype == MQ_FP16)
-        return d.fmt == MQ_FP4_NV ? run_narrow<true, __half>(d, p, rows, 16, c.split, false, stream)
-                                  : run_narrow<false, __half>(d, p, rows, 16, c.split, false, stream);
-    return d.fmt == MQ_FP4_NV ? run_narrow<true, __nv_bfloat16>(d, p, rows, 16, c.split, false, stream)
-                              : run_narrow<false, __nv_bfloat16>(d, p, rows, 16, c.split, false, stream);
+        return d.fmt == MQ_FP4_NV ? run_narrow<true, __half>(d, p, rows, c, false, stream)
+                                  : run_narrow<false, __half>(d, p, rows, c, false, stream);
+    return d.fmt == MQ_FP4_NV ? run_narrow<true, __nv_bfloat16>(d, p, rows, c, false, stream)
+                              : run_narrow<false, __nv_bfloat16>(d, p, rows, c, false, stream);
 }
 
 }  // namespace mq

@@ -62,3 +62,78 @@ def test_a_workspace_for_the_largest_batch_serves_the_smaller_ones(mq, cuda, fmt
             assert E > 1 or torch.equal(Y, w.linear(X, None, ws[:-64]))
         assert (ws[-64:] == 9).all()
     assert w.device_error() == 0
+
+
+class KernelNode(ctypes.Structure):  # CUDA_KERNEL_NODE_PARAMS
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                ("smem", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
+                ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+class Attribute(ctypes.Structure):  # CUlaunchAttribute
+    _fields_ = [("id", ctypes.c_int), ("pad", ctypes.c_int), ("value", ctypes.c_uint * 16)]
+
+
+class Config(ctypes.Structure):  # CUlaunchConfig
+    _fields_ = [("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3), ("smem", ctypes.c_uint),
+                ("stream", ctypes.c_void_p), ("attrs", ctypes.POINTER(Attribute)), ("count", ctypes.c_uint)]
+
+
+def launches(cu, stream, call):
+    """(kernel's name, CTAs of the launch, CTAs that the device holds at once)
+    of what a call launches, from the graph it leaves in a capture.
+
+    The runtime's own count of clusters takes an SM for one CTA of a kernel with
+    tensor memory. So many CTAs as an SM has registers and shared memory for
+    (228 KB, of which a CTA takes 1 KB more than it asks for) hold so many
+    clusters as that at least."""
+    ptr, CLUSTER = ctypes.c_void_p, 4
+    graph, count = ptr(), ctypes.c_size_t()
+    assert cu.cuStreamBeginCapture_v2(ptr(stream), 2) == 0
+    status = call()
+    assert cu.cuStreamEndCapture(ptr(stream), ctypes.byref(graph)) == 0 and status == 0
+    assert cu.cuGraphGetNodes(graph, None, ctypes.byref(count)) == 0
+    nodes = (ptr * count.value)()
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(count)) == 0
+    out = []
+    for node in nodes:
+        k, cluster, name, held = KernelNode(), (ctypes.c_uint * 16)(), ctypes.c_char_p(), ctypes.c_int()
+        assert cu.cuGraphKernelNodeGetParams_v2(ptr(node), ctypes.byref(k)) == 0
+        func = ptr(k.func)
+        if not k.func:
+            assert cu.cuKernelGetFunction(ctypes.byref(func), ptr(k.kern)) == 0
+        assert cu.cuFuncGetName(ctypes.byref(name), func) == 0
+        assert cu.cuGraphKernelNodeGetAttribute(ptr(node), CLUSTER, cluster) == 0
+        size = max(1, cluster[0])
+        a = Attribute(id=CLUSTER)
+        a.value[:3] = [size, 1, 1]
+        c = Config(grid=k.grid, block=k.block, smem=k.smem, stream=None, attrs=ctypes.pointer(a), count=1)
+        assert cu.cuOccupancyMaxActiveClusters(ctypes.byref(held), func, ctypes.byref(c)) == 0
+        regs = ctypes.c_int()
+        assert cu.cuFuncGetAttribute(ctypes.byref(regs), 4, func) == 0
+        share = min(228 * 1024 // (k.smem + 1024), 65536 // (regs.value * k.block[0])) if k.smem else 1
+        out.append((name.value.decode(), k.grid[0], held.value * size * share))
+    assert cu.cuGraphDestroy(graph) == 0
+    return out
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("N,K", [(1024, 4096), (1920, 2048), (2048, 2048), (2816, 8192), (4096, 11008), (9500, 1024),
+                                 (11008, 4096), (20480, 512), (28672, 2048), (37888, 512)])
+def test_products_of_few_tokens_run_in_one_wave(mq, cuda, fmt, N, K):
+    # clusters that find no room wait for all of the first ones to end
+    w = mq.Fp4Weight.pack(torch.zeros(N, K, dtype=BF16, device=cuda), fmt)
+    lib, cu, s = mq.lib(), ctypes.CDLL("libcuda.so.1"), torch.cuda.Stream().cuda_stream
+    X, Y = torch.zeros(128, K, dtype=BF16, device=cuda), torch.empty(128, N, dtype=BF16, device=cuda)
+    ws = torch.empty(max(16, w.workspace_bytes(128)), dtype=torch.uint8, device=cuda)
+    for M in (1, 8, 16, 17, 24, 32, 33, 48, 64, 65, 100, 128):
+        def call():
+            return lib.mq_fp4_linear(w.handle, X.data_ptr(), 0, M, K, Y.data_ptr(), N, ws.data_ptr(), ws.numel(), s)
+
+        assert call() == 0  # sets the kernel up
+        torch.cuda.synchronize()
+        got = [x for x in launches(cu, s, call) if "quantize" not in x[0]]
+        assert len(got) == 1
+        name, ctas, held = got[0]
+        assert "fp4_narrow" in name or "fp4_wide" in name
+        assert ctas <= held, (M, name, ctas, held)
