@@ -70,6 +70,7 @@ struct Fp4Device {
     int64_t E = 0, N = 0, K = 0;
     int fmt = 0;
     int device = 0, sms = 0;
+    int clusters[9] = {};  // clusters of 1 to 8 narrow CTAs that the device holds at once, one CTA an SM
     int KS = 0;      // K stages
     int64_t NT = 0;  // 128-row tiles of one matrix
     uint8_t *pieces = nullptr;
@@ -104,6 +105,9 @@ mq_status launch_fp4_order(const Fp4Device &d, uint8_t *codes, uint8_t *scales, 
 // offsets were there.
 mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t *offsets, void *Y,
                             mq_dtype dtype, int64_t ldy, bool chained, cudaStream_t stream);
+
+// Fills in d.clusters for d's format and device (the current one).
+mq_status fp4_count_clusters(Fp4Device &d);
 
 // The same from X as it is (as for launch_fp4_quantize), quantised by the
 // product itself, where fp4_linear_quantises says that this is the faster way.

@@ -89,6 +89,7 @@ mq_status allocate(mq_fp4_weight *w, int64_t E, int64_t N, int64_t K, int fmt) {
     d.sms = sm_count();
     d.KS = static_cast<int>((K + kFp4StageK - 1) / kFp4StageK);
     d.NT = (N + 127) / 128;
+    if (mq_status st = fp4_count_clusters(d)) return st;
     auto get = [&](void **p, int64_t bytes) {
         const cudaError_t e = cudaMalloc(p, static_cast<size_t>(bytes));
         if (e != cudaSuccess) return fp4_cuda_fail(e, "cudaMalloc");

@@ -20,6 +20,7 @@
 // quantised by every CTA alike.
 
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "fp4.h"
@@ -475,7 +476,7 @@ Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
     // CTAs of up to 16 tokens share an SM, so that the next launch's may start
     // beside them. More tokens leave a CTA its SM, and a ring of up to eight
     // slots, as long as all clusters run at once that way: the SMs' groups hold
-    // only so many, and the others wait for the first to end (nvfp4 24 x 2048 x
+    // only so many (148, 74, 45, 33, 26, 22, 15, 15 of 1 to 8 CTAs), and the others wait for the first to end (nvfp4 24 x 2048 x
     // 2048, 16 tiles: 9.4 us with 8 CTAs a cluster, 6.3 us with 6). Where they do
     // not, up to 32 tokens two share an SM if each then has four slots, which
     // nvfp4 with partial sums has not; else K is split less. One an SM and two,
@@ -483,8 +484,7 @@ Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
     // (224) 32.2 and 25.9; mxfp4 24 x 11008 x 4096 8.9 and 10.4, 48 x 8192 x 8192
     // 13.8 and 16.1.
     int each = per <= 16 ? 2 : 1;
-    constexpr int kClusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};  // of 1 to 8 CTAs, one an SM
-    while (each == 1 && likely > kClusters[split]) {
+    while (each == 1 && likely > d.clusters[split]) {
         if (per <= 32 && narrow_stages(d.fmt, TT, split, 2) >= 4)
             each = 2;
         else if (split > 1)
@@ -578,6 +578,42 @@ mq_status launch_fp4_linear(const Fp4Device &d, const Fp4Rows &x, const int32_t 
     p.fp16 = dtype == MQ_FP16;
     return d.fmt == MQ_FP4_NV ? run_narrow<true, void>(d, p, x.rows, c, chained, stream)
                               : run_narrow<false, void>(d, p, x.rows, c, chained, stream);
+}
+
+template <bool NV>
+static mq_status count_clusters(Fp4Device &d) {
+    // asked for once a device: it does not change
+    static std::mutex lock;
+    static int counts[64][9] = {};
+    const std::lock_guard<std::mutex> hold(lock);
+    int *of = counts[d.device];
+    if (!of[1]) {
+        const auto kernel = fp4_narrow_kernel<NV, void>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        for (int size = 8; size > 0 && e == cudaSuccess; --size) {
+            cudaLaunchAttribute attr = {};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = size;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(size * d.sms);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = 227 * 1024;  // one CTA an SM
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&of[size], kernel, &cfg);
+        }
+        if (e != cudaSuccess) {
+            of[1] = 0;
+            return fp4_cuda_fail(e, "fp4 weight: device setup");
+        }
+    }
+    std::copy(of, of + 9, d.clusters);
+    return MQ_OK;
+}
+
+mq_status fp4_count_clusters(Fp4Device &d) {
+    return d.fmt == MQ_FP4_NV ? count_clusters<true>(d) : count_clusters<false>(d);
 }
 
 // Ordered for the wide form, whose four loader warps then have nothing to

@@ -137,3 +137,26 @@ def test_products_of_few_tokens_run_in_one_wave(mq, cuda, fmt, N, K):
         name, ctas, held = got[0]
         assert "fp4_narrow" in name or "fp4_wide" in name
         assert ctas <= held, (M, name, ctas, held)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_clusters_fill_the_device_once(mq, cuda, fmt):
+    # every number of row tiles around what the device holds of clusters of 2
+    # to 8 CTAs, whatever its SMs' groups are like
+    lib, cu, s, K = mq.lib(), ctypes.CDLL("libcuda.so.1"), torch.cuda.Stream().cuda_stream, 6144
+    X, most = torch.zeros(48, K, dtype=BF16, device=cuda), 0
+    for tiles in [*range(1, 40), *range(42, 52), *range(70, 80)]:
+        N = 128 * tiles
+        w = mq.Fp4Weight.pack(torch.zeros(N, K, dtype=BF16, device=cuda), fmt)
+        Y = torch.empty(48, N, dtype=BF16, device=cuda)
+        ws = torch.empty(max(16, w.workspace_bytes(48)), dtype=torch.uint8, device=cuda)
+        for M in (24, 48):
+            def call():
+                return lib.mq_fp4_linear(w.handle, X.data_ptr(), 0, M, K, Y.data_ptr(), N, ws.data_ptr(), ws.numel(), s)
+
+            assert call() == 0
+            torch.cuda.synchronize()
+            name, ctas, held = [x for x in launches(cu, s, call) if "quantize" not in x[0]][0]
+            assert ctas <= held, (M, tiles, name, ctas, held)
+            most = max(most, ctas)
+    assert most > 0.9 * torch.cuda.get_device_properties(cuda).multi_processor_count
