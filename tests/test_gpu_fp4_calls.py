@@ -3,10 +3,11 @@ launch, on the GPU."""
 
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_fp4 import BF16, FMTS, values
+from test_gpu_fp4 import BF16, FMTS, held, values
 
 pytestmark = pytest.mark.gpu
 
@@ -97,7 +98,7 @@ def launches(cu, stream, call):
     assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(count)) == 0
     out = []
     for node in nodes:
-        k, cluster, name, held = KernelNode(), (ctypes.c_uint * 16)(), ctypes.c_char_p(), ctypes.c_int()
+        k, cluster, name, room = KernelNode(), (ctypes.c_uint * 16)(), ctypes.c_char_p(), ctypes.c_int()
         assert cu.cuGraphKernelNodeGetParams_v2(ptr(node), ctypes.byref(k)) == 0
         func = ptr(k.func)
         if not k.func:
@@ -108,11 +109,11 @@ def launches(cu, stream, call):
         a = Attribute(id=CLUSTER)
         a.value[:3] = [size, 1, 1]
         c = Config(grid=k.grid, block=k.block, smem=k.smem, stream=None, attrs=ctypes.pointer(a), count=1)
-        assert cu.cuOccupancyMaxActiveClusters(ctypes.byref(held), func, ctypes.byref(c)) == 0
+        assert cu.cuOccupancyMaxActiveClusters(ctypes.byref(room), func, ctypes.byref(c)) == 0
         regs = ctypes.c_int()
         assert cu.cuFuncGetAttribute(ctypes.byref(regs), 4, func) == 0
         share = min(228 * 1024 // (k.smem + 1024), 65536 // (regs.value * k.block[0])) if k.smem else 1
-        out.append((name.value.decode(), k.grid[0], held.value * size * share))
+        out.append((name.value.decode(), k.grid[0], room.value * size * share))
     assert cu.cuGraphDestroy(graph) == 0
     return out
 
@@ -134,9 +135,9 @@ def test_products_of_few_tokens_run_in_one_wave(mq, cuda, fmt, N, K):
         torch.cuda.synchronize()
         got = [x for x in launches(cu, s, call) if "quantize" not in x[0]]
         assert len(got) == 1
-        name, ctas, held = got[0]
+        name, ctas, room = got[0]
         assert "fp4_narrow" in name or "fp4_wide" in name
-        assert ctas <= held, (M, name, ctas, held)
+        assert ctas <= room, (M, name, ctas, room)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -156,7 +157,46 @@ def test_clusters_fill_the_device_once(mq, cuda, fmt):
 
             assert call() == 0
             torch.cuda.synchronize()
-            name, ctas, held = [x for x in launches(cu, s, call) if "quantize" not in x[0]][0]
-            assert ctas <= held, (M, tiles, name, ctas, held)
+            name, ctas, room = [x for x in launches(cu, s, call) if "quantize" not in x[0]][0]
+            assert ctas <= room, (M, tiles, name, ctas, room)
             most = max(most, ctas)
     assert most > 0.9 * torch.cuda.get_device_properties(cuda).multi_processor_count
+
+
+def exact_values(q):
+    """The values held, in 64 bits on the device (exact: 2, 4 and 24 bits)."""
+    c = torch.stack([q.codes & 15, q.codes >> 4], -1).flatten(-2)[:, :q.K].long()
+    half = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=c.device)
+    v = half[c & 7] * (1 - 2 * (c >> 3))
+    if q.fmt == "mxfp4":
+        s = torch.exp2(q.scales.double() - 127)
+    else:
+        s = q.scales.view(torch.float8_e4m3fn).double() * q.row_scale.double()[:, None]
+    return v * s.repeat_interleave(32 if q.fmt == "mxfp4" else 16, dim=1)[:, :q.K]
+
+
+def test_exact_values(mq, cuda):
+    for fmt in FMTS:
+        X = values(50, 333, BF16, 1)
+        assert np.array_equal(exact_values(mq.fp4_quantize(X.to(cuda), fmt)).cpu().numpy(), held(X, fmt))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [BF16, torch.float16])
+@pytest.mark.parametrize("M,N,K", [(1, 8192, 11008), (16, 14336, 4096), (24, 20480, 4100), (60, 4096, 11008),
+                                   (96, 4096, 4096), (1000, 4096, 2048), (2048, 2560, 4096), (2000, 9001, 11008),
+                                   (4096, 4096, 11008)])
+def test_every_output_of_large_products(mq, cuda, fmt, dtype, M, N, K):
+    # all of them against 64 bits, within the bound of a single output: a block
+    # of 16 columns left out of such products is beyond it in most outputs (two
+    # of three at K = 11008, nine of ten at 4096)
+    X = values(M, K, dtype, M, spread=0.3).to(cuda)
+    w = mq.Fp4Weight.pack((values(N, K, torch.float32, N, spread=0.3) * 0.05).to(cuda), fmt)
+    x64, w64 = exact_values(mq.fp4_quantize(X, fmt)), exact_values(w.export())
+    y64, S = x64 @ w64.T, x64.abs() @ w64.abs().T
+    # as `bound`, with the 64-bit products' own error, 2^-53 of S for each of K terms
+    tol = ((torch.finfo(dtype).eps / 2 + 2**-22) * y64.abs() + (K / 16 + 16) * 2.0**-23 * S * 1.01 + K * 2.0**-52 * S +
+           2.0**-25)
+    off = (w.linear(X).double() - y64).abs()
+    assert (off <= tol).all()
+    assert w.device_error() == 0
