@@ -428,8 +428,10 @@ mq_status mq_fp4_quantize(const void *X_dev, mq_dtype dtype, int64_t rows, int64
                           const int32_t *index, int64_t x_rows, mq_fp4_format fmt, void *codes,
                           void *scales, float *row_scale, mq_stream stream);
 
-/* The values of a quantised matrix, rounded once to dtype, into Y (row stride
- * ldy >= K elements). Errors as mq_fp4_quantize. */
+/* The values of a quantised matrix as 32-bit floats, rounded to dtype, into Y
+ * (row stride ldy >= K elements). The 32-bit values are exact for MQ_FP4_MX;
+ * for MQ_FP4_NV code * scale is exact and the product with the row factor is
+ * rounded, so that a 16-bit Y is rounded twice. Errors as mq_fp4_quantize. */
 mq_status mq_fp4_dequantize(const void *codes, const void *scales, const float *row_scale,
                             int64_t rows, int64_t K, mq_fp4_format fmt, void *Y_dev, mq_dtype dtype,
                             int64_t ldy, mq_stream stream);
@@ -462,9 +464,10 @@ int64_t mq_fp4_workspace_bytes(const mq_fp4_weight *w, int64_t rows);
  * is quantised to the weight's format into `workspace` (16-byte aligned, at
  * least mq_fp4_workspace_bytes(w, M), not shared with a concurrent call) and
  * multiplied on the tensor cores' 4-bit path: exact products of codes and
- * scales, fp32 accumulation, Y [M][N] of X's type, stride ldy >= N, each
- * element rounded once. Asynchronous, no allocation; results do not depend on
- * timing. Y must not overlap X or the workspace. M = 0 launches nothing.
+ * scales, fp32 accumulation, MQ_FP4_NV's two row factors in two products that
+ * are rounded to 32 bits, then a rounding to Y [M][N] of X's type, stride ldy
+ * >= N. Asynchronous, no allocation; results do not depend on timing. Y must
+ * not overlap X or the workspace. M = 0 launches nothing.
  * mq_fp4_linear_codes takes X already quantised to the weight's format, for
  * an X that several weights share.
  * Errors: INVALID_ARG for NULL, misaligned or too small buffers, strides

@@ -200,3 +200,14 @@ def test_every_output_of_large_products(mq, cuda, fmt, dtype, M, N, K):
     off = (w.linear(X).double() - y64).abs()
     assert (off <= tol).all()
     assert w.device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [BF16, torch.float16])
+@pytest.mark.parametrize("K", [999, 4096])
+def test_dequantised_values_are_rounded_as_documented(mq, cuda, fmt, dtype, K):
+    # to 32 bits by the row factor (not at all for mxfp4), then to the type
+    q = mq.fp4_quantize(values(700, K, BF16, 1).to(cuda), fmt)
+    whole, once = q.dequantize(), exact_values(q).float()
+    assert torch.equal(whole, once)
+    assert torch.equal(q.dequantize(dtype), once.to(dtype))
