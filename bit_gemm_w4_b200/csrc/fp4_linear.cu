@@ -468,21 +468,25 @@ Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
     const int64_t sms = d.sms;
     const int64_t likely = mats * d.NT;
     const int TT = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : static_cast<int>((per + 15) / 16 * 16);
-    // K is split as far as that gives every SM at most one CTA: past it the
-    // further CTAs start after the first ones' loads (1 x 4096 x 4096 takes
-    // 9.1, 8.0, 8.5 and 9.3 us with 2, 4, 6 and 8; 1 x 11008 x 4096, 86 tiles,
-    // 11.8 us with 1 and 14.0 us with 4).
+    // Times below: us on the device, calls in a row over weights that L2 does not
+    // hold, quantisation included, nvfp4 unless another format is named.
+    // K is split as far as that gives every SM at most one CTA (1 x 4096 x 4096,
+    // 32 tiles: 7.6, 6.3, 6.5 and 6.8 with 2, 4, 6 and 8). For one token of 75 to
+    // 148 tiles that is less than would be best: 1 x 11008 x 4096 (86 tiles) takes
+    // 10.9, 9.5, 8.8 and 13.6 with 1 to 4.
     int split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d.KS, sms / likely})));
     // CTAs of up to 16 tokens share an SM, so that the next launch's may start
     // beside them. More tokens leave a CTA its SM, and a ring of up to eight
     // slots, as long as all clusters run at once that way: the SMs' groups hold
-    // only so many (148, 74, 45, 33, 26, 22, 15, 15 of 1 to 8 CTAs), and the others wait for the first to end (nvfp4 24 x 2048 x
-    // 2048, 16 tiles: 9.4 us with 8 CTAs a cluster, 6.3 us with 6). Where they do
-    // not, up to 32 tokens two share an SM if each then has four slots, which
-    // nvfp4 with partial sums has not; else K is split less. One an SM and two,
-    // in us: nvfp4 24 x 11008 x 4096 (86 tiles) 10.2 and 11.8, 24 x 28672 x 8192
-    // (224) 32.2 and 25.9; mxfp4 24 x 11008 x 4096 8.9 and 10.4, 48 x 8192 x 8192
-    // 13.8 and 16.1.
+    // only so many (148, 74, 45, 33, 26, 22, 15, 15 of 1 to 8 CTAs), and the others
+    // wait for the first to end (24 x 2048 x 2048, 16 tiles: 9.4 with 8 CTAs a
+    // cluster, 6.3 with 6). Where they do not, up to 32 tokens two share an SM if
+    // each then has four slots, which nvfp4 with partial sums has not; else K is
+    // split less. One an SM and two: 24 x 11008 x 4096 (86 tiles) 10.2 and 11.8, 24
+    // x 28672 x 8192 (224) 32.2 and 25.9; mxfp4 24 x 11008 x 4096 8.9 and 10.4, 48
+    // x 8192 x 8192 13.8 and 16.1. (Up to 16 tokens too a lone CTA would be better
+    // for large layers, 1 x 16384 x 8192 16.1 and 18.5, and worse for small ones,
+    // 1 x 4096 x 4096 6.8 and 6.3.)
     int each = per <= 16 ? 2 : 1;
     while (each == 1 && likely > d.clusters[split]) {
         if (per <= 32 && narrow_stages(d.fmt, TT, split, 2) >= 4)
@@ -493,15 +497,14 @@ Choice choose(const Fp4Device &d, int64_t rows, bool grouped) {
             break;
     }
     // Up to 32 tokens: narrow, as long as its tiles run in one wave of two CTAs
-    // an SM (16 x 28672 x 8192, 224 tiles: 24.1 us, wide 27.0; 192 rows over 64
-    // experts of 2048 x 2048, 1024 tiles: 28.0 us, wide 25.0). Up to 128: where
+    // an SM (mxfp4 16 x 28672 x 8192, 224 tiles: 23.5, wide 28.0; 192 rows over 64
+    // experts of 2048 x 2048, 1024 tiles: 34.2, wide 32.1). Up to 128: where
     // splitting K, which the wide form does not do, takes enough stages off a
-    // CTA to pay for the sum, whose time goes with the tokens. nvfp4 with its
-    // quantisation, narrow and wide: 80 x 4096 x 11008 (43 stages, 11 a CTA)
-    // 14.1 and 19.6 us, 128 tokens 16.4 and 20.9; 80 x 1024 x 4096 (16, 2) 8.3
-    // and 9.5, 128 tokens 9.9 and 10.0; 48 x 4096 x 4096 (16, 4) 9.0 and 9.8,
-    // 80 tokens 10.6 and 10.3. More than one tile of tokens gains nothing (192
-    // x 4096 x 11008 20.7 and 21.3).
+    // CTA to pay for the sum, whose time goes with the tokens. Narrow and wide:
+    // 80 x 4096 x 11008 (43 stages, 11 a CTA) 13.7 and 19.0, 128 tokens 16.0 and
+    // 20.5; 80 x 1024 x 4096 (16, 2) 8.1 and 9.3, 128 tokens 9.7 and 9.8; 48 x 4096
+    // x 4096 (16, 4) 8.8 and 9.7, 80 tokens 10.4 and 10.2. Not with a second tile
+    // of tokens, whose clusters find no room (192 x 4096 x 11008 27.3 and 21.0).
     const int64_t saved = d.KS - (d.KS + split - 1) / split;
     const bool narrow = per <= 32 ? likely <= 2 * sms : per <= kMaxTT && 6 * saved >= per;
     return {narrow ? TT : 0, split, each, likely, per};
@@ -617,9 +620,9 @@ mq_status fp4_count_clusters(Fp4Device &d) {
 }
 
 // Ordered for the wide form, whose four loader warps then have nothing to
-// place: 2048 x 14336 x 4096 nvfp4, at the power limit, takes 76 us instead of
-// 92 us (with the quantisation). Not for many matrices with few rows each,
-// whose slots would be mostly empty.
+// place: 2048 x 14336 x 4096 nvfp4 takes 62 us instead of 76 us, 4096 x 4096 x
+// 11008 mxfp4 98 us instead of 102 us (with the quantisation). Not for many
+// matrices with few rows each, whose slots would be mostly empty.
 static bool ordered(const Fp4Device &d, int64_t rows, int HT) { return d.E <= 8 * (rows / HT) + 256; }
 
 static Fp4Order token_order(const Fp4Device &d, int64_t rows, int HT) {
@@ -660,9 +663,10 @@ int64_t fp4_token_scale_bytes(const Fp4Device &d, int64_t rows) {
 // through memory saved against every CTA's own quantisation, which for
 // MQ_FP4_NV includes a look at the whole of each row. It is taken where it
 // costs the device at most 2 us more (nvfp4 4096 x 4096, 1 / 4 / 8 / 16 rows:
-// 6.3 / 7.4 / 9.2 / 13.4 us against 6.7 / 6.8 / 7.2 / 7.6 us; mxfp4 4.7 / 4.9 /
-// 6.0 / 7.6 against 5.8 / 5.8 / 6.1 / 6.4 us): the host's share of a launch is
-// 3 us. A CTA with more stages than its ring (11008 x 4096) quantises while
+// 6.3 / 7.3 / 9.0 / 12.9 us against 6.5 / 6.6 / 7.0 / 7.3 us; mxfp4 4.7 / 5.0 /
+// 5.9 / 7.5 against 5.9 / 6.0 / 6.3 / 6.5 us): the host's share of a launch is
+// 3 us. (In a captured graph the host has none, and those up to 2 us are lost.) A
+// CTA with more stages than its ring (11008 x 4096) quantises while
 // its loads wait, and large weights leave no time to hide it in.
 bool fp4_linear_quantises(const Fp4Device &d, int64_t rows) {
     const Choice c = choose(d, rows, d.E > 1);

@@ -201,8 +201,8 @@ mq_status pick_quantize(const QuantArgs &a, cudaStream_t stream) {
     };
     // Chunks a thread: one while all of them find a thread at once, two up to
     // some waves of that, then four (nvfp4, one / two / four: 999 x 2891 4.5 /
-    // 5.0 / 6.7 us, 2048 x 4096 7.2 / 6.2 / 6.9 us, 8192 x 4096 23.0 / 18.8 /
-    // 17.3 us); no more than a row has for a warp.
+    // 5.1 / 6.7 us, 2048 x 4096 7.2 / 6.1 / 6.8 us, 8192 x 4096 23.0 / 17.8 /
+    // 17.1 us); no more than a row has for a warp.
     const long long total = a.rows * chunks;
     if (chunks <= 32 || (chunks <= 512 && total <= 1350ll * sm_count())) return run_quantize<T, NV, 1>(a, threads(1), stream);
     if (chunks <= 64 || (chunks <= 1024 && total <= 7000ll * sm_count())) return run_quantize<T, NV, 2>(a, threads(2), stream);

@@ -463,8 +463,8 @@ Fp4WidePlan fp4_wide_plan(const Fp4Device &d, int64_t rows) {
     // for each of them; the constants (ns) fit 8192^3, 4096 x 4096 x 11008 and
     // 2048 x 14336 x 4096 at 128 to 384 tokens, all of which run at the power
     // limit. Two halves move less and pay 1 us a tile, for which K has to be
-    // long: 8192^3 mxfp4 takes 274 us with 384 tokens and 291 us with 224, 2048
-    // x 14336 x 4096 nvfp4 85 and 76 us (both with the quantisation).
+    // long: 8192^3 mxfp4 takes 253 us with 384 tokens and 275 us with 224, 2048
+    // x 14336 x 4096 nvfp4 80 and 63 us (both with the quantisation).
     // Matrices of a ragged batch end half a tile early on average.
     const bool nv = d.fmt == MQ_FP4_NV;
     const int64_t NT = (d.NT + 1) / 2, pairs = d.sms / 2, mats = std::min<int64_t>(d.E, rows);

@@ -792,7 +792,8 @@ class Fp4Weight:
 
     def linear(self, X, Y=None, workspace=None, *, dtype=None, stream=None):
         """Y = X @ W^T. X: a bf16 or fp16 [M, K] tensor, quantised within the
-        call into the workspace (workspace_bytes(M) bytes), with Y of its
+        call into the workspace (workspace_bytes(M) bytes: a size for M rows
+        serves fewer too), with Y of its
         type; or an Fp4Tensor, with Y of `dtype` (Y's own or bf16 unless given)."""
         index = self._index
         if stream is not None or _t.current_device() != index:

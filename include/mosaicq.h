@@ -469,7 +469,10 @@ int64_t mq_fp4_workspace_bytes(const mq_fp4_weight *w, int64_t rows);
  * >= N. Asynchronous, no allocation; results do not depend on timing. Y must
  * not overlap X or the workspace. M = 0 launches nothing.
  * mq_fp4_linear_codes takes X already quantised to the weight's format, for
- * an X that several weights share.
+ * an X that several weights share. It saves the quantisation, but not the
+ * ordering of the scales, which mq_fp4_linear leaves to its quantisation: for
+ * MQ_FP4_NV and thousands of rows that costs more than it saves (on a B200 2048
+ * x 14336 x 4096 takes 68 us from codes, 62 us from X).
  * Errors: INVALID_ARG for NULL, misaligned or too small buffers, strides
  * below the widths, a handle of several matrices or a current device other
  * than the handle's; UNSUPPORTED for fp32 or more than 2^30 rows; CUDA when a
