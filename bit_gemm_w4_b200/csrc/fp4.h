@@ -131,8 +131,8 @@ struct Fp4WidePlan {
 };
 Fp4WidePlan fp4_wide_plan(const Fp4Device &d, int64_t rows);
 // Its tiles, the smallest first, and whether up to `rows` rows may take tile i:
-// not where every smaller count of rows fits as many of the tiles before it,
-// which take less time each.
+// not where they make no more of the tile before it, which takes less time (one
+// for a single matrix; for several the plan counts half a tile each, one at least).
 constexpr int kFp4WideTiles[] = {32, 64, 96, 128, 160, 192, 224, 256, 320, 384};
 inline int fp4_wide_halves(int TT) { return TT > 224 ? 2 : 1; }
 inline int fp4_scale_unit(int HT) { return HT > 128 ? 1024 : 512; }
